@@ -92,7 +92,8 @@ typedef enum hhr_status {
   HHR_ERR_UNSUPPORTED = 2, /* valid but outside the supported sizes above    */
   HHR_ERR_WORKSPACE = 3,   /* workspace pointer null or smaller than needed  */
   HHR_ERR_CUDA = 4,        /* a CUDA call or kernel launch failed            */
-  HHR_ERR_TIMEOUT = 5      /* a bounded inter-CTA wait ran out (device flag) */
+  HHR_ERR_TIMEOUT = 5,     /* a bounded inter-CTA wait ran out (device flag) */
+  HHR_ERR_BAD_INDEX = 6    /* a page, sequence or length out of range (device flag) */
 } hhr_status;
 
 /* Largest number of pages per (sequence, KV head) a decode call accepts. */
@@ -290,10 +291,10 @@ int32_t hhr_decode_step_noalloc(const hhr_dims* dims, const void* q, const float
 int32_t hhr_noalloc_read_status(void* stream);
 
 /*
- * Waits for `stream`, returns the workspace status word (HHR_OK or
- * HHR_ERR_TIMEOUT) and clears it.  After HHR_ERR_TIMEOUT the workspace must be
- * zero-filled again before the next call.  Returns HHR_ERR_CUDA if the copy
- * or the wait fails.
+ * Waits for `stream`, returns the workspace status word (HHR_OK,
+ * HHR_ERR_TIMEOUT, or HHR_ERR_BAD_INDEX from the paged calls) and clears it.
+ * After HHR_ERR_TIMEOUT the workspace must be zero-filled again before the
+ * next call.  Returns HHR_ERR_CUDA if the copy or the wait fails.
  */
 int32_t hhr_read_status(void* workspace, void* stream);
 
@@ -318,6 +319,178 @@ int32_t hhr_read_status(void* workspace, void* stream);
  * concurrent use.
  */
 int32_t hhr_test_arm_timeout(int32_t where, uint64_t spin_cycles);
+
+/* ------------------------------------------------------------------------
+ * The dense serving path: rotary positions, the append to a paged key-value
+ * cache, and the attention of one new token over it.  These calls serve what
+ * stands next to the retrieval path in a model: keys reach a cache rotated
+ * (the paper's models use rotary positions), and the layers that the paper
+ * leaves dense (§4.1) attend over every key of sequences of different
+ * lengths.  No counterpart in the paper's own method.  Conventions (memory,
+ * streams, errors, dependent launch) as above; none of these kernels waits
+ * for another CTA.
+ * ------------------------------------------------------------------------ */
+
+/* Element types. */
+#define HHR_TYPE_BF16 0
+#define HHR_TYPE_F16 1
+#define HHR_TYPE_F32 2
+#define HHR_TYPE_E4M3 3 /* 8-bit float (4 exponent, 3 mantissa bits, max 448), cache only */
+
+/* hhr_rotation.flags */
+#define HHR_ROPE_INTERLEAVED 1 /* pairs (2j, 2j+1) instead of (j, j + rot/2)   */
+#define HHR_ROPE_TRANSPOSE 2   /* the transposed rotation: the gradient of a
+                                  rotation with respect to its input          */
+
+typedef struct hhr_rotation {
+  int32_t rot;   /* leading elements of a head that are rotated: even, 0 .. d */
+  int32_t flags; /* 0, or an OR of the HHR_ROPE_* above                       */
+  float mscale;  /* factor on the rotated elements (1 for none)               */
+} hhr_rotation;
+
+/* Ways of stretching the frequencies to long contexts (hhr_rope_freqs). */
+#define HHR_ROPE_SCALE_NONE 0
+#define HHR_ROPE_SCALE_LINEAR 1 /* f / factor                                     */
+#define HHR_ROPE_SCALE_NTK 2    /* base * factor^(rot / (rot - 2))                */
+#define HHR_ROPE_SCALE_YARN 3   /* per-pair ramp between f and f / factor over the
+                                   pair index, mscale = 0.1 ln(factor) + 1        */
+#define HHR_ROPE_SCALE_BANDS 4  /* the same between two wavelengths (Llama 3.1)    */
+
+typedef struct hhr_rope_scaling {
+  int32_t kind;  /* HHR_ROPE_SCALE_*                                              */
+  int32_t orig;  /* YARN, BANDS: context length the model was first trained on     */
+  double base;   /* frequency base, > 1                                           */
+  double factor; /* stretch, >= 1 (ignored by NONE)                               */
+  double low;    /* YARN, BANDS: pairs with fewer turns over `orig` are stretched  */
+  double high;   /* YARN, BANDS: pairs with more turns are left (low < high)       */
+} hhr_rope_scaling;
+
+/*
+ * Rotary frequencies: writes rot/2 doubles (radians per position) to the HOST
+ * array freqs and the factor for hhr_rotation.mscale to *mscale (host).
+ *   NONE    f_j = base^(-2j/rot)
+ *   LINEAR  f_j / factor
+ *   NTK     f_j with base * factor^(rot/(rot-2))  (rot > 2)
+ *   YARN    with dim(t) = rot ln(orig / (2 pi t)) / (2 ln base), lo = max(floor(dim(high)), 0),
+ *           hi = min(ceil(dim(low)), rot/2 - 1) and s_j = clamp((j - lo) / max(hi - lo, 0.001), 0, 1):
+ *           f_j (1 - s_j) + f_j / factor * s_j; mscale = 0.1 ln(factor) + 1
+ *   BANDS   with turns_j = orig f_j / (2 pi) and s_j = clamp((turns_j - low) / (high - low), 0, 1):
+ *           f_j / factor * (1 - s_j) + f_j s_j
+ * A host call: enqueues nothing.
+ */
+int32_t hhr_rope_freqs(const hhr_rope_scaling* scaling, int32_t rot, double* freqs, float* mscale);
+
+/*
+ * Rotary positions: for token t, head h and pair j, with the angle
+ * a = pos[t] * freqs[j],
+ *   y1 = mscale * (x1 cos a - x2 sin a),  y2 = mscale * (x2 cos a + x1 sin a)
+ * (HHR_ROPE_TRANSPOSE: sin a with the other sign), where (x1, x2) are the
+ * pair's elements; elements from rot on are copied.  The angle and its
+ * remainder modulo a turn are formed in float64, so far positions lose
+ * nothing; the rotation runs in float32 and is rounded once.
+ *   T, H, d  tokens, heads, head dimension: d even, 2 <= d <= 512, T * H < 2^31.
+ *   type     HHR_TYPE_BF16, _F16 or _F32, of x and y.
+ *   freqs    device, read: f64 [rot/2].  pos device, read: i32 [T], any sign.
+ *   x, y     device: element e of head h of token t at [t * tok + h * head + e]
+ *            (strides in elements, >= 0; y's rows must not overlap).  y == x with
+ *            the same strides rotates in place; any other overlap is an
+ *            error of the caller.
+ * T == 0 or H == 0 enqueues nothing.
+ */
+int32_t hhr_rope(int32_t T, int32_t H, int32_t d, int32_t type, const hhr_rotation* rotation,
+                 const double* freqs, const int32_t* pos, const void* x, int64_t x_tok,
+                 int64_t x_head, void* y, int64_t y_tok, int64_t y_head, void* stream);
+
+/*
+ * A paged key-value cache.  Element e of head g of the token at offset i of
+ * page p is K[p * k_page + g * k_head + i * k_tok + e] (V likewise), so pages
+ * may be token-major, head-major or a view of a larger buffer: the caches of
+ * hhr_dims are the case page = n_cap, table[b] = {b}.  A sequence's token n is
+ * at offset n % page of page table[b * table_stride + n / page].
+ * With HHR_TYPE_E4M3 a stored element stands for k_scale (v_scale) times its value.
+ * Supported: d in {64, 128, 256}; Hq % Hkv == 0; q_type BF16 or F16; kv_type
+ * q_type or E4M3; page >= 1; table_cols * page < 2^31; strides > 0 and a
+ * multiple of 16 bytes.
+ */
+typedef struct hhr_paged {
+  int32_t Hq;           /* query heads                                     */
+  int32_t Hkv;          /* key/value heads                                 */
+  int32_t d;            /* head dimension                                  */
+  int32_t page;         /* tokens per page                                 */
+  int32_t n_pages;      /* pages in the pool                               */
+  int32_t table_cols;   /* pages a sequence may have                       */
+  int32_t table_stride; /* elements between two sequences' rows of `table` */
+  int32_t q_type;       /* queries, and the keys and values appended       */
+  int32_t kv_type;      /* cache elements                                  */
+  float k_scale;        /* E4M3: > 0; otherwise 1                          */
+  float v_scale;
+  int32_t reserved;     /* 0 */
+  int64_t k_page, k_head, k_tok; /* strides of K in elements               */
+  int64_t v_page, v_head, v_tok;
+} hhr_paged;
+
+/*
+ * Appends T new tokens to a paged cache: rotates their keys (as hhr_rope does,
+ * rounded once to the cache's type), stores keys and values, and optionally
+ * rotates the same tokens' queries; one launch.
+ *   T, B     tokens, rows of `table`.
+ *   rotation, freqs  as for hhr_rope, no TRANSPOSE; rotation NULL (or rot 0): no rotation.
+ *   pos      device, read: i32 [T], the token's place in its sequence.  A
+ *            negative place is a padding row: nothing of that token is written.
+ *   rope_pos device, read, nullable: i32 [T] positions for the angles (NULL: pos).
+ *   seq      device, read, nullable: i32 [T] row of `table` (NULL: token t is of
+ *            sequence t; T <= B).
+ *   table    device, read: i32 [B][table_stride].
+ *   q, q_out device, nullable together: [T][Hq][d] with q_tok / q_out_tok elements
+ *            between tokens; q_out == q with the same stride rotates in place.
+ *   k, v     device, read: [T][Hkv][d] with k_row / v_row elements between tokens.
+ *   K, V     device, write: the pools.  Rows that no token names stay as they were.
+ *            Two tokens of one call must not name the same place.
+ *   status   device, nullable: u32 word set to HHR_ERR_BAD_INDEX when a token's
+ *            sequence, place or page is out of range; nothing of that token is
+ *            written.  (The first word of an hhr_paged_attend workspace serves,
+ *            read with hhr_read_status.)
+ * E4M3: a value is multiplied by 1 / scale in float32 and rounded once, saturating at +-448.
+ */
+int32_t hhr_paged_append(const hhr_paged* cache, int32_t T, int32_t B,
+                         const hhr_rotation* rotation, const double* freqs, const int32_t* pos,
+                         const int32_t* rope_pos, const int32_t* seq, const int32_t* table,
+                         const void* q, int64_t q_tok, void* q_out, int64_t q_out_tok,
+                         const void* k, int64_t k_row, const void* v, int64_t v_row, void* K,
+                         void* V, uint32_t* status, void* stream);
+
+/*
+ * Bytes of device workspace hhr_paged_attend needs for this cache on the
+ * current device; 0 if the cache is invalid.  Zero-filled once before its
+ * first use, left in that state by every call; not to be shared by two calls
+ * that may run at the same time (two captured graphs included).  It does not
+ * depend on the number of sequences or their lengths.
+ */
+size_t hhr_paged_workspace_size(const hhr_paged* cache);
+
+/*
+ * Attention of one new token per sequence over a paged cache:
+ *   out[b][h] = sum_n softmax_n(scale * q[b][h].K[n]) V[n],
+ *   lse[b][h] = ln sum_n exp(scale * q[b][h].K[n])
+ * over the tokens max(0, lens[b] - window) <= n < lens[b] of head h's KV group
+ * (window 0: all).  A sequence without tokens gets zeros and lse = -inf.  What
+ * lies in the cache beyond a sequence's tokens is not read.  Sums and softmax
+ * statistics are float32; results do not depend on the order in which CTAs run.
+ *   q        device, read: [B][Hq][d] of q_type, q_seq elements between sequences
+ *            (16-byte aligned rows).
+ *   table    device, read: i32 [B][table_stride].  lens device, read: i32 [B].
+ *   out      device, write: [B][Hq][d] of out_type (q_type or HHR_TYPE_F32).
+ *   lse      device, write, nullable: f32 [B][Hq].
+ *   workspace device: at least hhr_paged_workspace_size(cache) bytes.
+ * Lengths and pages are read on the device, so a captured call follows them.
+ * A length outside [0, table_cols * page] counts as 0 and a page outside
+ * [0, n_pages) as masked tokens; either sets the workspace status word to
+ * HHR_ERR_BAD_INDEX (hhr_read_status) and leaves the workspace usable.
+ */
+int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64_t q_seq,
+                         const void* K, const void* V, const int32_t* table, const int32_t* lens,
+                         int32_t window, float scale, int32_t out_type, void* out, float* lse,
+                         void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -20,6 +20,7 @@ HHR_ERR_UNSUPPORTED = 2
 HHR_ERR_WORKSPACE = 3
 HHR_ERR_CUDA = 4
 HHR_ERR_TIMEOUT = 5
+HHR_ERR_BAD_INDEX = 6
 HHR_MAX_PAGES = 16384
 HHR_NOALLOC_SCRATCH_BYTES = 4 << 20
 
@@ -48,10 +49,37 @@ def make_dims(B, Hq, Hkv, d, bits, page, n_cap, flags=0) -> hhr_dims:
     return hhr_dims(B, Hq, Hkv, d, bits, page, n_cap, flags)
 
 
+HHR_TYPE_BF16, HHR_TYPE_F16, HHR_TYPE_F32, HHR_TYPE_E4M3 = 0, 1, 2, 3
+HHR_ROPE_INTERLEAVED = 1   # pairs (2j, 2j+1) instead of (j, j + rot/2)
+HHR_ROPE_TRANSPOSE = 2     # the transposed rotation (the gradient)
+HHR_ROPE_SCALE_NONE, HHR_ROPE_SCALE_LINEAR, HHR_ROPE_SCALE_NTK = 0, 1, 2
+HHR_ROPE_SCALE_YARN, HHR_ROPE_SCALE_BANDS = 3, 4
+
+
+class hhr_rotation(C.Structure):
+    _fields_ = [("rot", C.c_int32), ("flags", C.c_int32), ("mscale", C.c_float)]
+
+
+class hhr_rope_scaling(C.Structure):
+    _fields_ = [("kind", C.c_int32), ("orig", C.c_int32), ("base", C.c_double), ("factor", C.c_double),
+                ("low", C.c_double), ("high", C.c_double)]
+
+
+class hhr_paged(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("Hq", "Hkv", "d", "page", "n_pages", "table_cols", "table_stride",
+                                         "q_type", "kv_type")] + \
+               [("k_scale", C.c_float), ("v_scale", C.c_float), ("reserved", C.c_int32)] + \
+               [(n, C.c_int64) for n in ("k_page", "k_head", "k_tok", "v_page", "v_head", "v_tok")]
+
+    def __repr__(self):
+        return "hhr_paged(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
 _lib = None
 
 _P = C.c_void_p
 _I32 = C.c_int32
+_I64 = C.c_int64
 _SIGS = {
     "hhr_version": (_I32, []),
     "hhr_status_string": (C.c_char_p, [_I32]),
@@ -73,6 +101,14 @@ _SIGS = {
     "hhr_noalloc_read_status": (_I32, [_P]),
     "hhr_encode_status": (_I32, [_P]),
     "hhr_test_arm_timeout": (_I32, [_I32, C.c_uint64]),
+    "hhr_rope_freqs": (_I32, [C.POINTER(hhr_rope_scaling), _I32, _P, C.POINTER(C.c_float)]),
+    "hhr_rope": (_I32, [_I32, _I32, _I32, _I32, C.POINTER(hhr_rotation), _P, _P, _P, _I64, _I64, _P, _I64, _I64,
+                        _P]),
+    "hhr_paged_append": (_I32, [C.POINTER(hhr_paged), _I32, _I32, C.POINTER(hhr_rotation), _P, _P, _P, _P, _P,
+                                _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P]),
+    "hhr_paged_workspace_size": (C.c_size_t, [C.POINTER(hhr_paged)]),
+    "hhr_paged_attend": (_I32, [C.POINTER(hhr_paged), _I32, _P, _I64, _P, _P, _P, _P, _I32, C.c_float, _I32, _P,
+                                _P, _P, C.c_size_t, _P]),
 }
 
 
@@ -221,7 +257,7 @@ def hhr_decode_step_noalloc(dims, q, R, W, codes, meta, K, V, n_valid, P, k, sca
 
 
 def hhr_read_status(workspace, stream=None) -> int:
-    """Device status word of a workspace (HHR_OK or HHR_ERR_TIMEOUT), cleared after reading."""
+    """Device status word of a workspace (HHR_OK, HHR_ERR_TIMEOUT, HHR_ERR_BAD_INDEX), cleared after reading."""
     st = lib().hhr_read_status(_ptr(workspace), _stream(stream))
     if st == HHR_ERR_CUDA:
         raise HhrError(st, "hhr_read_status")
@@ -247,3 +283,35 @@ def hhr_encode_status(stream=None) -> int:
 def hhr_test_arm_timeout(where, spin_cycles) -> None:
     """Test hook: the next matching call's bounded waits run out (see hhr.h)."""
     _check(lib().hhr_test_arm_timeout(where, spin_cycles), "hhr_test_arm_timeout")
+
+
+def hhr_rope_freqs(scaling, rot):
+    """(frequencies, mscale): rot/2 Python floats in radians per position, and the factor of hhr_rotation."""
+    out, mscale = (C.c_double * max(rot // 2, 1))(), C.c_float()
+    _check(lib().hhr_rope_freqs(C.byref(scaling), rot, C.addressof(out), C.byref(mscale)), "hhr_rope_freqs")
+    return list(out), mscale.value
+
+
+def hhr_rope(T, H, d, type, rotation, freqs, pos, x, x_tok, x_head, y, y_tok, y_head, stream=None) -> None:
+    _check(lib().hhr_rope(T, H, d, type, C.byref(rotation), _ptr(freqs), _ptr(pos), _ptr(x), x_tok, x_head,
+                          _ptr(y), y_tok, y_head, _stream(stream)), "hhr_rope")
+
+
+def hhr_paged_append(cache, T, B, rotation, freqs, pos, rope_pos, seq, table, q, q_tok, q_out, q_out_tok,
+                     k, k_row, v, v_row, K, V, status=None, stream=None) -> None:
+    _check(lib().hhr_paged_append(C.byref(cache), T, B, None if rotation is None else C.byref(rotation),
+                                  _ptr(freqs), _ptr(pos), _ptr(rope_pos), _ptr(seq), _ptr(table), _ptr(q), q_tok,
+                                  _ptr(q_out), q_out_tok, _ptr(k), k_row, _ptr(v), v_row, _ptr(K), _ptr(V),
+                                  _ptr(status), _stream(stream)), "hhr_paged_append")
+
+
+def hhr_paged_workspace_size(cache) -> int:
+    return lib().hhr_paged_workspace_size(C.byref(cache))
+
+
+def hhr_paged_attend(cache, B, q, q_seq, K, V, table, lens, window, scale, out_type, out, lse=None,
+                     workspace=None, ws_bytes=None, stream=None) -> None:
+    ws_bytes = _nbytes(workspace) if ws_bytes is None and workspace is not None else (ws_bytes or 0)
+    _check(lib().hhr_paged_attend(C.byref(cache), B, _ptr(q), q_seq, _ptr(K), _ptr(V), _ptr(table), _ptr(lens),
+                                  window, scale, out_type, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
+                                  _stream(stream)), "hhr_paged_attend")

@@ -7,6 +7,7 @@ library with a static CUDA runtime.
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
@@ -17,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhhr.so")
-SOURCES = ["api.cu", "decode.cu", "encode.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "decode.cu", "encode.cu", "noalloc.cu", "paged.cu", "rope.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
            "-I", INCLUDE, "-I", CSRC]
@@ -33,6 +34,20 @@ def _deps() -> list[str]:
     files.append(os.path.join(INCLUDE, "hhr.h"))
     files.append(os.path.abspath(__file__))
     return files
+
+
+def _src_deps(src: str) -> list[str]:
+    """A source file and the files of this tree it includes, directly or not."""
+    seen, todo = [], [os.path.join(CSRC, src)]
+    while todo:
+        f = todo.pop()
+        if f in seen:
+            continue
+        seen.append(f)
+        with open(f) as fh:
+            names = re.findall(r'^#include "([^"]+)"', fh.read(), flags=re.M)
+        todo += [p for n in names for p in (os.path.join(CSRC, n), os.path.join(INCLUDE, n)) if os.path.exists(p)]
+    return seen + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
@@ -51,6 +66,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
+        if not force and os.path.exists(obj) and all(os.path.getmtime(f) < os.path.getmtime(obj)
+                                                     for f in _src_deps(src)):
+            return obj
         cmd = [nvcc, *ARCH, *NVFLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:

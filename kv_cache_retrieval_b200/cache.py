@@ -11,6 +11,7 @@ import math
 import torch
 
 from . import _binding as B
+from .paged import HHRPagedCache
 
 
 class HHRCache:
@@ -39,11 +40,43 @@ class HHRCache:
             raise B.HhrError(B.HHR_ERR_INVALID_ARG, "hhr_workspace_size")
         self.workspace = torch.zeros(ws, dtype=torch.uint8, device=dev)
         self.scale = 1.0 / math.sqrt(head_dim)
+        self._paged = None
 
     # -- key encoding -------------------------------------------------------
     def encode(self, n_begin, n_end, stream=None):
         B.hhr_encode_keys(self.dims, self.K, self.R, self.W, n_begin, n_end, self.codes,
                           self.meta, stream)
+
+    # -- the dense serving calls over the same keys and values ---------------
+    def paged(self):
+        """(cache, table): K and V as an HHRPagedCache whose page is a whole sequence, and its table [batch, 1];
+        attention with a length for each sequence, and the layers that are kept dense, go through it."""
+        if self._paged is None:
+            d = self.dims
+            self._paged = (HHRPagedCache(q_heads=d.Hq, kv_heads=d.Hkv, page=d.n_cap, head_dim=d.d, K=self.K, V=self.V),
+                           torch.arange(d.B, dtype=torch.int32, device=self.device).view(d.B, 1))
+        return self._paged
+
+    def append(self, k, v, n_begin, *, q=None, freqs=None, interleaved=False, mscale=1.0):
+        """Takes tokens n_begin .. n_begin + n of every sequence on the current stream: k, v bf16
+        [batch, n, kv_heads, head_dim] as the projection leaves them.  Their keys are rotated by their places
+        (freqs: rope_freqs; None: as they are), stored with the values, and encoded.  Returns q [batch, n, q_heads,
+        head_dim] rotated by the same places, or None."""
+        d = self.dims
+        paged, table = self.paged()
+        if k.dim() != 4 or k.shape[0] != d.B or v.dim() != 4 or v.shape[:2] != k.shape[:2] or \
+                (q is not None and (q.dim() != 4 or q.shape[:2] != k.shape[:2])):
+            raise ValueError(f"k, v, q: expected [{d.B}, tokens, heads, {d.d}]")
+        n = k.shape[1]
+        if n_begin < 0 or n_begin + n > d.n_cap:
+            raise ValueError(f"tokens {n_begin} .. {n_begin + n} of a capacity of {d.n_cap}")
+        pos = torch.arange(n_begin, n_begin + n, dtype=torch.int32, device=self.device).repeat(d.B)
+        seq = table.expand(d.B, n).reshape(-1)
+        rows = [None if t is None else t.flatten(0, 1) for t in (k, v, q)]
+        out = paged.append(rows[0], rows[1], pos, table, seq=seq, q=rows[2], freqs=freqs, interleaved=interleaved,
+                           mscale=mscale)
+        self.encode(n_begin, n_begin + n)
+        return None if q is None else out.view(q.shape)
 
     # -- decode -------------------------------------------------------------
     def select(self, q, n_valid, dbg_U=None, dbg_D=None, stream=None):

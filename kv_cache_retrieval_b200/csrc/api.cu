@@ -16,7 +16,7 @@ namespace {
 
 using namespace hhr;
 
-constexpr int32_t kVersion = 100;  // 0.1.0
+constexpr int32_t kVersion = 200;  // 0.2.0
 
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
@@ -207,6 +207,7 @@ const char* hhr_status_string(int32_t status) {
     case HHR_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case HHR_ERR_CUDA: return "CUDA error";
     case HHR_ERR_TIMEOUT: return "bounded inter-CTA wait timed out";
+    case HHR_ERR_BAD_INDEX: return "page, sequence or length out of range";
     default: return "unknown status";
   }
 }
