@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhhr.so")
-SOURCES = ["api.cu", "decode.cu", "encode.cu", "noalloc.cu", "paged.cu", "rope.cu"]
+SOURCES = ["api.cu", "decode.cu", "encode.cu", "noalloc.cu", "paged.cu", "paged_bf16.cu", "paged_bf16_e4m3.cu",
+           "paged_f16.cu", "paged_f16_e4m3.cu", "rope.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
            "-I", INCLUDE, "-I", CSRC]

@@ -1,112 +1,19 @@
-// Attention of one new token per sequence over a paged key-value cache.
-//
-// One CTA per (sequence, query head): its warps take the tokens in turn, each
-// with its own running maximum, sum and output (float32), merged at the end
-// in the order of the warps.
+// hhr_paged_attend: checks, workspace and launch (the kernel: paged_attend.cuh).
 
-#include <algorithm>
-#include <cfloat>
 #include <cstring>
 
-#include "hhr_internal.cuh"
-#include "paged_common.cuh"
+#include "paged_attend.cuh"
 
 namespace hhr {
 namespace {
 
-constexpr int kPagedThreads = 256;
-constexpr int kPagedWarps = kPagedThreads / 32;
+// Workspace: status word, counters, exchanged states.
+constexpr size_t kPagedCounters = 256;
+constexpr size_t kPagedParts = kPagedCounters + (kPagedMaxGrid * sizeof(uint32_t) + 255) / 256 * 256;
 
-struct PagedArgs {
-  const void* q;
-  const void* K;
-  const void* V;
-  const int32_t* table;
-  const int32_t* lens;
-  void* out;
-  float* lse;
-  uint32_t* status;
-  int64_t q_seq, k_page, k_head, k_tok, v_page, v_head, v_tok;
-  float scale_log2, v_scale;
-  int B, Hq, Hkv, page, n_pages, table_cols, table_stride, window, out_f32;
-};
-
-template <typename TQ, typename TC, int D>
-__global__ void __launch_bounds__(kPagedThreads) paged_kernel(const PagedArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float s_m[kPagedWarps], s_l[kPagedWarps], s_o[kPagedWarps][D];
-  const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq, g = h / (a.Hq / a.Hkv);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  dependency_wait();
-  launch_dependents();
-  int len = a.lens[b];
-  if (len < 0 || len > static_cast<int64_t>(a.table_cols) * a.page) {
-    if (threadIdx.x == 0) *a.status = HHR_ERR_BAD_INDEX;
-    len = 0;
-  }
-  const int lo = a.window ? max(0, len - a.window) : 0;
-  float q[E], o[E], m = -INFINITY, l = 0;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = to_f32(static_cast<const TQ*>(a.q)[b * a.q_seq + h * D + e * 32 + lane]);
-    o[e] = 0;
-  }
-  for (int n = lo + warp; n < len; n += kPagedWarps) {
-    const int id = a.table[static_cast<int64_t>(b) * a.table_stride + n / a.page];
-    if (id < 0 || id >= a.n_pages) {
-      *a.status = HHR_ERR_BAD_INDEX;
-      continue;
-    }
-    const TC* k = static_cast<const TC*>(a.K) + id * a.k_page + g * a.k_head + (n % a.page) * a.k_tok;
-    const TC* v = static_cast<const TC*>(a.V) + id * a.v_page + g * a.v_head + (n % a.page) * a.v_tok;
-    float x = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x = fmaf(q[e], to_f32(k[e * 32 + lane]), x);
-#pragma unroll
-    for (int w = 16; w; w >>= 1) x += __shfl_xor_sync(~0u, x, w);
-    x *= a.scale_log2;
-    const float mn = fmaxf(m, x), base = mn == -INFINITY ? 0.0f : mn;
-    const float c = exp2f(m - base), p = exp2f(x - base);
-    m = mn;
-    l = l * c + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], c, p * to_f32(v[e * 32 + lane]));
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = o[e];
-  __syncthreads();
-  float M = -INFINITY, L = 0;
-  for (int w = 0; w < kPagedWarps; ++w) M = fmaxf(M, s_m[w]);
-  const float base = M == -INFINITY ? 0.0f : M;
-  for (int w = 0; w < kPagedWarps; ++w) L += s_l[w] * exp2f(s_m[w] - base);
-  const float inv = L > 0 ? a.v_scale / L : (L == 0 ? 0.0f : L);
-  for (int e = threadIdx.x; e < D; e += kPagedThreads) {
-    float y = 0;
-    for (int w = 0; w < kPagedWarps; ++w) y += s_o[w][e] * exp2f(s_m[w] - base);
-    y *= inv;
-    const size_t at = (static_cast<size_t>(b) * a.Hq + h) * D + e;
-    if (a.out_f32)
-      static_cast<float*>(a.out)[at] = y;
-    else
-      static_cast<TQ*>(a.out)[at] = from_f32<TQ>(y);
-  }
-  if (threadIdx.x == 0 && a.lse)
-    a.lse[static_cast<size_t>(b) * a.Hq + h] = L == 0 ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
-}
-
-template <typename TQ, typename TC>
-cudaError_t launch_paged(const PagedArgs& a, int d, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.B) * a.Hq);
-  switch (d) {
-    case 64: return launch_dependent<PagedArgs>(paged_kernel<TQ, TC, 64>, grid, kPagedThreads, 0, s, a);
-    case 128: return launch_dependent<PagedArgs>(paged_kernel<TQ, TC, 128>, grid, kPagedThreads, 0, s, a);
-    default: return launch_dependent<PagedArgs>(paged_kernel<TQ, TC, 256>, grid, kPagedThreads, 0, s, a);
-  }
-}
+// Query heads of a unit: the heads of a KV head in equal chunks of at most paged_max_heads.
+int unit_chunks(const hhr_paged& c) { return (c.Hq / c.Hkv + paged_max_heads(c.d) - 1) / paged_max_heads(c.d); }
+int unit_heads(const hhr_paged& c) { return (c.Hq / c.Hkv + unit_chunks(c) - 1) / unit_chunks(c); }
 
 }  // namespace
 }  // namespace hhr
@@ -115,7 +22,11 @@ using namespace hhr;
 
 extern "C" {
 
-size_t hhr_paged_workspace_size(const hhr_paged* cache) { return check_paged(cache) == HHR_OK ? 256 : 0; }
+size_t hhr_paged_workspace_size(const hhr_paged* cache) {
+  if (check_paged(cache) != HHR_OK) return 0;
+  const size_t part = paged_part_stride(unit_heads(*cache), cache->d);
+  return align_up(kPagedParts + 2 * kPagedMaxGrid * part * sizeof(float), 256);
+}
 
 int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64_t q_seq,
                          const void* K, const void* V, const int32_t* table, const int32_t* lens,
@@ -142,7 +53,10 @@ int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64
   a.lens = lens;
   a.out = out;
   a.lse = lse;
-  a.status = static_cast<uint32_t*>(workspace);
+  char* const ws = static_cast<char*>(workspace);
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.counters = reinterpret_cast<uint32_t*>(ws + kPagedCounters);
+  a.parts = reinterpret_cast<float*>(ws + kPagedParts);
   a.q_seq = q_seq;
   a.k_page = c.k_page;
   a.k_head = c.k_head;
@@ -161,14 +75,24 @@ int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64
   a.table_stride = c.table_stride;
   a.window = window;
   a.out_f32 = out_type == HHR_TYPE_F32;
+  a.r = c.Hq / c.Hkv;
+  a.chunk = unit_heads(c);
+  a.chunks = unit_chunks(c);
+  a.part_stride = paged_part_stride(a.chunk, c.d);
+  while ((int64_t{1} << a.page_shift) < c.page) ++a.page_shift;
+  a.page_magic = static_cast<uint32_t>((((uint64_t{1} << a.page_shift) - c.page) << 32) / c.page + 1);
+  a.min_tiles = 8;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return HHR_ERR_CUDA;
+  const int grid = std::min(sms, kPagedMaxGrid);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = c.kv_type == HHR_TYPE_E4M3;
   cudaError_t e;
   if (c.q_type == HHR_TYPE_BF16)
-    e = c.kv_type == HHR_TYPE_E4M3 ? launch_paged<__nv_bfloat16, __nv_fp8_e4m3>(a, c.d, s)
-                                   : launch_paged<__nv_bfloat16, __nv_bfloat16>(a, c.d, s);
+    e = e4m3 ? launch_paged_bf16_e4m3(a, c.d, grid, s) : launch_paged_bf16(a, c.d, grid, s);
   else
-    e = c.kv_type == HHR_TYPE_E4M3 ? launch_paged<__half, __nv_fp8_e4m3>(a, c.d, s)
-                                   : launch_paged<__half, __half>(a, c.d, s);
+    e = e4m3 ? launch_paged_f16_e4m3(a, c.d, grid, s) : launch_paged_f16(a, c.d, grid, s);
   return e == cudaSuccess ? HHR_OK : HHR_ERR_CUDA;
 }
 
