@@ -24,8 +24,8 @@ extern "C" {
 
 size_t hhr_paged_workspace_size(const hhr_paged* cache) {
   if (check_paged(cache) != HHR_OK) return 0;
-  const size_t part = paged_part_stride(unit_heads(*cache), cache->d);
-  return align_up(kPagedParts + 2 * kPagedMaxGrid * part * sizeof(float), 256);
+  const size_t state = paged_state(unit_heads(*cache), cache->d);
+  return align_up(kPagedParts + (2 + 8) * kPagedMaxGrid * state * sizeof(float), 256);
 }
 
 int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64_t q_seq,
@@ -78,10 +78,11 @@ int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64
   a.r = c.Hq / c.Hkv;
   a.chunk = unit_heads(c);
   a.chunks = unit_chunks(c);
-  a.part_stride = paged_part_stride(a.chunk, c.d);
+  a.state = paged_state(a.chunk, c.d);
+  a.firsts = a.parts + static_cast<size_t>(2 * kPagedMaxGrid) * a.state;
   while ((int64_t{1} << a.page_shift) < c.page) ++a.page_shift;
   a.page_magic = static_cast<uint32_t>((((uint64_t{1} << a.page_shift) - c.page) << 32) / c.page + 1);
-  a.min_tiles = 8;
+  a.min_tiles = 1;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return HHR_ERR_CUDA;
