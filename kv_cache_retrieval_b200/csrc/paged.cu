@@ -37,6 +37,8 @@ int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64
   if (B < 0 || window < 0 || !std::isfinite(scale)) return HHR_ERR_INVALID_ARG;
   if (out_type != c.q_type && out_type != HHR_TYPE_F32) return HHR_ERR_INVALID_ARG;
   if (static_cast<int64_t>(B) * c.Hq >= (int64_t{1} << 31)) return HHR_ERR_UNSUPPORTED;
+  // tiles of the call x warps of the card stay below 2^63
+  if (static_cast<double>(B) * c.Hq * (static_cast<double>(c.table_cols) * c.page / 16 + 1) >= 0x1p51) return HHR_ERR_UNSUPPORTED;
   if (!workspace || !aligned_to(workspace, 256) || ws_bytes < hhr_paged_workspace_size(cache)) return HHR_ERR_WORKSPACE;
   if (B == 0) return HHR_OK;
   if (!q || !K || !V || !table || !lens || !out) return HHR_ERR_INVALID_ARG;
@@ -82,7 +84,7 @@ int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64
   a.firsts = a.parts + static_cast<size_t>(2 * kPagedMaxGrid) * a.state;
   while ((int64_t{1} << a.page_shift) < c.page) ++a.page_shift;
   a.page_magic = static_cast<uint32_t>((((uint64_t{1} << a.page_shift) - c.page) << 32) / c.page + 1);
-  a.min_tiles = 1;
+  a.min_tiles = 4;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return HHR_ERR_CUDA;

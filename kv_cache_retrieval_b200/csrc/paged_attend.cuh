@@ -84,8 +84,7 @@ struct PagedShape {
   static constexpr int kRingWarp = kDepth * 2 * kTile;            // of a warp; in the end it holds the warp's last state
   static constexpr int kQ = kRing + kWarps * kRingWarp;
   static constexpr int kQWarp = kQRegs ? 0 : kHeads * D * 2;
-  // the join: weights of 8 heads, their inverse sums, the threads' sums
-  static constexpr int kJoin = (8 * kPagedMaxGrid + 8 + 4 * kThreads) * 4;
+  static constexpr int kJoin = kThreads * 24;                     // the threads' sums, maxima and weight sums in the join
   static constexpr int kMasks = kQ + std::max(kWarps * kQWarp, kJoin);
   static constexpr int kSmem = kMasks + kWarps * kDepth * 4;
   static_assert(kSmem <= 226 * 1024, "shared memory of a CTA");
@@ -130,8 +129,7 @@ struct TileCursor {
 
 // An open state: one of several of its unit.
 struct OpenState {
-  int64_t x0, x1;       // the unit's tiles
-  const float* at;
+  int64_t x0, x1;       // the unit's tiles; x1 = 0: none
   int b, u;
 };
 
@@ -141,8 +139,19 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+// Copies of K and V: read once, so L2 lets them go first and keeps tables, exchanged states and code.
+__device__ __forceinline__ uint64_t read_once() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t policy, bool live) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0),
+               "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -198,18 +207,25 @@ __device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& 
   }
 }
 
-// The two e4m3 values of the low (high) half of x as fp16, exactly.
-__device__ __forceinline__ uint32_t wide_lo(uint32_t x) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x & 0xffffu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// Four e4m3 values as fp16, exactly: the low and the high pair.  (The header's conversion of a pair goes through two
+// 16-bit halves and takes 3.6 cycles an SM for four values, this form 1.5.)
+__device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
 }
-__device__ __forceinline__ uint32_t wide_hi(uint32_t x) { return wide_lo(x >> 16); }
 
-// Byte offset of 16-byte chunk c of row i in a tile of rows of `row` bytes: eight rows read at the same chunk, or one
-// row's chunks, fall on different banks.
+// Tiles lie in shared memory as rows of `row` bytes whose 16-byte chunk c stands at c ^ (i & 7) in row i (at
+// c ^ ((i >> 1) & 3) in rows of 64 bytes): eight rows read at the same chunk, or one row's chunks, fall on different
+// banks.  The lowest bits of a row and a chunk go through turn(); the rest of both are added, so that the addresses of a
+// tile differ from a few lane-owned ones by constants.
 template <int row>
-__device__ __forceinline__ int swizzled(int i, int c) {
+__device__ __forceinline__ int turn(int i, int c) {
   return i * row + ((c ^ (row >= 128 ? (i & 7) : ((i >> 1) & 3))) << 4);
+}
+template <int row>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t turned, int c) {   // turned + chunk c, where turned has chunk 0 or 1
+  return (turned ^ ((c & 7) << 4)) + (c >> 3) * 128;
 }
 
 // The weight of a state of maximum m among states of maximum top; 1 / sum of a unit's weights (0 for none, NaN stays)
@@ -231,9 +247,9 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
   // weights up to 2^14 in fp16: it keeps 2^-38 of the largest
   constexpr float kLift = std::is_same<TM, __half>::value ? 14.0f : 0.0f;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int64_t s_scan[kWarps];
+  __shared__ int64_t s_scan[kWarps], s_before[kThreads];
+  __shared__ int s_seqs[kWarps], s_last[2];
   __shared__ OpenState s_open[2 * kWarps];   // of a warp: of the unit it ends, of the unit it leaves unfinished
-  __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
   const int units = a.Hkv * a.chunks;
@@ -241,89 +257,88 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
   dependency_wait();
   launch_dependents();
 
-  // Rows of sequences without tokens, and lengths out of range.
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const int len = a.lens[b];
-    if (len < 0 || len > a.table_cols * a.page) {
-      if (tid == 0) *a.status = HHR_ERR_BAD_INDEX;
-    } else if (len > 0) {
-      continue;
+  // The tiles before each run of `per` sequences: in the lanes of every warp where 32 hold them, or in shared memory.
+  const bool few = a.B <= 32;
+  const int per = few ? 1 : (a.B + kThreads - 1) / kThreads;
+  int64_t total, before = 0;
+  int n_seqs;          // sequences with tokens
+  if (few) {
+    int mine = 0;
+    if (lane < a.B) {
+      const TileRange t = tile_range<kTokens>(a, lane);
+      mine = max(0, t.end - t.first);
     }
-    const size_t row = static_cast<size_t>(b) * a.Hq;
-    for (int e = tid; e < a.Hq * D; e += kThreads) {
-      if (a.out_f32)
-        static_cast<float*>(a.out)[row * D + e] = 0.0f;
-      else
-        static_cast<TQ*>(a.out)[row * D + e] = from_f32<TQ>(0.0f);
-    }
-    if (a.lse)
-      for (int h = tid; h < a.Hq; h += kThreads) a.lse[row + h] = -INFINITY;
-  }
-
-  // The tiles of all units; thread i sums those of its run of sequences.
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int b_lo = min(tid * per, a.B), b_hi = min(b_lo + per, a.B);
-  int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) {
-    const TileRange t = tile_range<kTokens>(a, b);
-    mine += max(0, t.end - t.first);
-  }
-  int64_t upto = mine;
+    int64_t upto = mine;
 #pragma unroll
-  for (int w = 1; w < 32; w <<= 1) {
-    const int64_t x = __shfl_up_sync(~0u, upto, w);
-    if (lane >= w) upto += x;
+    for (int w = 1; w < 32; w <<= 1) {
+      const int64_t x = __shfl_up_sync(~0u, upto, w);
+      if (lane >= w) upto += x;
+    }
+    total = __shfl_sync(~0u, upto, 31);
+    before = upto - mine;
+    n_seqs = __popc(__ballot_sync(~0u, mine > 0));
+  } else {
+    const int b_lo = min(tid * per, a.B), b_hi = min(b_lo + per, a.B);
+    int64_t mine = 0;
+    int seqs = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const TileRange t = tile_range<kTokens>(a, b);
+      mine += max(0, t.end - t.first);
+      seqs += t.end > t.first;
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+      const int64_t x = __shfl_up_sync(~0u, upto, w);
+      if (lane >= w) upto += x;
+    }
+    seqs = __reduce_add_sync(~0u, seqs);
+    if (lane == 31) {
+      s_scan[warp] = upto;
+      s_seqs[warp] = seqs;
+    }
+    __syncthreads();
+    total = 0;
+    n_seqs = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) upto += s_scan[w];
+      total += s_scan[w];
+      n_seqs += s_seqs[w];
+    }
+    s_before[tid] = upto - mine;
   }
-  if (lane == 31) s_scan[warp] = upto;
-  s_open[tid % (2 * kWarps)].x1 = 0;
+  if (tid < 2 * kWarps) s_open[tid].x1 = 0;
   __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += s_scan[w];
   total *= units;
-  const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(int64_t{1}, total / (kWarps * a.min_tiles))));
+  // G CTAs take part.  Where that is not all of them it is a multiple of the units, so that equal ones are not shared.
+  int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(int64_t{1}, total / (kWarps * a.min_tiles))));
+  if (G < gridDim.x && static_cast<int64_t>(n_seqs) * units <= G) G -= G % (n_seqs * units);
   const int c = blockIdx.x;
-  if (total == 0 || c >= G) return;
-  // warp i of the G kWarps takes [first_of(i), first_of(i + 1))
-  const int64_t quot = total / (G * kWarps);
-  const int rem = static_cast<int>(total % (G * kWarps));
-  const auto first_of = [&](int i) { return quot * i + min(i, rem); };
-  const auto cta_of = [&](int64_t x) {
-    const int64_t wide = rem * (quot + 1);
-    return static_cast<int>(x < wide ? x / (quot + 1) : rem + (x - wide) / quot) / kWarps;
+  // warp i of the G kWarps takes [first_of(i), first_of(i + 1)) (the host bounds total * G * kWarps)
+  const uint32_t n_warps = G * kWarps;
+  const auto first_of = [&](int i) { return static_cast<int64_t>(static_cast<uint64_t>(total) * i / n_warps); };
+  const auto cta_of = [&](int64_t x) {   // the CTA whose range holds x
+    return static_cast<int>((static_cast<uint64_t>(x + 1) * n_warps - 1) / static_cast<uint64_t>(total)) / kWarps;
   };
   const int64_t f0 = first_of(c * kWarps), f1 = first_of((c + 1) * kWarps);
-  const int64_t w0 = first_of(c * kWarps + warp), w1 = first_of(c * kWarps + warp + 1);
+  const int64_t w0 = first_of(c * kWarps + warp), w1 = c < G ? first_of(c * kWarps + warp + 1) : w0;
 
   if (w0 < w1) {
-    // ---- where w0 lies: the run of sequences by the sums, then the sequence
+    // ---- where w0 lies: the last run that begins at or before it, then the sequence
     TileCursor seg;    // the unit being attended
-    int64_t pre = 0;
     {
-      int run = 0;
+      int64_t pre;
+      if (few) {
+        seg.b = __popc(__ballot_sync(~0u, before * units <= w0)) - 1;
+        pre = __shfl_sync(~0u, before, seg.b);
+      } else {
+        int run = -1;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {   // the run's warp
-        if (w0 >= (pre + s_scan[w]) * units && w + 1 < kWarps && run == 32 * w) {
-          pre += s_scan[w];
-          run = 32 * (w + 1);
-        }
+        for (int w = 0; w < kWarps; ++w) run += __popc(__ballot_sync(~0u, s_before[32 * w + lane] * units <= w0));
+        pre = s_before[run];
+        seg.b = run * per;
       }
-      // the run: lane i sums run i of that warp again
-      const int lo = min((run + lane) * per, a.B), hi = min(lo + per, a.B);
-      int64_t sum = 0;
-      for (int b = lo; b < hi; ++b) {
-        const TileRange t = tile_range<kTokens>(a, b);
-        sum += max(0, t.end - t.first);
-      }
-      int64_t end = sum;
-#pragma unroll
-      for (int w = 1; w < 32; w <<= 1) {
-        const int64_t x = __shfl_up_sync(~0u, end, w);
-        if (lane >= w) end += x;
-      }
-      const int at = __ffs(__ballot_sync(~0u, w0 < (pre + end) * units)) - 1;
-      pre += __shfl_sync(~0u, end - sum, at);
-      seg.b = (run + at) * per;
       for (;; ++seg.b) {
         seg.t = tile_range<kTokens>(a, seg.b);
         const int n = max(0, seg.t.end - seg.t.first);
@@ -346,8 +361,10 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
     constexpr int kCopies = kTokens / kRows;
     const int row0 = lane / kChunks, chunk0 = lane % kChunks;
     const bool whole = (a.page & 15) == 0;           // 16 rows do not cross pages
-    const unsigned char* const Kb = static_cast<const unsigned char*>(a.K) + chunk0 * 16;
-    const unsigned char* const Vb = static_cast<const unsigned char*>(a.V) + chunk0 * 16;
+    const int64_t k_page = a.k_page * kSize, k_tok = a.k_tok * kSize, k_head = a.k_head * kSize;   // bytes
+    const int64_t v_page = a.v_page * kSize, v_tok = a.v_tok * kSize, v_head = a.v_head * kSize;
+    const unsigned char* const Kb = static_cast<const unsigned char*>(a.K) + chunk0 * 16 + row0 * k_tok;
+    const unsigned char* const Vb = static_cast<const unsigned char*>(a.V) + chunk0 * 16 + row0 * v_tok;
     TileCursor ld = seg;
     int64_t ld_left = w1 - w0;   // tiles that have not been asked for
     const unsigned char *Kh = Kb, *Vh = Vb;   // of the tile's KV head
@@ -367,32 +384,38 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
       if (ask) id = a.table[static_cast<int64_t>(ld.b) * a.table_stride + p];
       mask = rows & kAll;
       const int kv = a.chunks == 1 ? ld.u : ld.u / a.chunks;
-      Kh = Kb + kv * a.k_head * kSize;
-      Vh = Vb + kv * a.v_head * kSize;
+      Kh = Kb + kv * k_head;
+      Vh = Vb + kv * v_head;
     };
+    const uint64_t policy = read_once();
+    const uint32_t lane_c = turn<kRow>(row0, chunk0);
+    const auto copy_to = [&](uint32_t dst, int j) { return dst + (lane_c ^ ((j * kRows & 7) << 4)) + j * kRows * kRow; };
     const auto copy_rows = [&](uint32_t dst, const unsigned char* base, int64_t page, int64_t tok) {
       if (whole) {
+        const int64_t step = tok * kRows;
 #pragma unroll
         for (int m = 0; m < kSub; ++m) {
-          const int64_t mid = kSub == 1 ? id : __shfl_sync(~0u, id, 16 * m);
-          const int64_t min_page = kSub == 1 ? in_page : __shfl_sync(~0u, in_page, 16 * m);
-          const unsigned char* src = base + (mid * page + (min_page + row0) * tok) * kSize;
-          const int64_t step = tok * (kRows * kSize);
-          const bool full = ((live >> (16 * m)) & 0xffffu) == 0xffffu;
+          const int mid = kSub == 1 ? id : __shfl_sync(~0u, id, 16 * m);
+          const int off = kSub == 1 ? in_page : __shfl_sync(~0u, in_page, 16 * m);
+          const unsigned char* src = base + (mid * page + off * tok);
+          constexpr int kEach = kCopies / kSub;
+          if (live == kAll) {
 #pragma unroll
-          for (int j = 0; j < kCopies / kSub; ++j) {
-            const int row = m * 16 + j * kRows + row0;
-            copy16(dst + swizzled<kRow>(row, chunk0), src, full || ((live >> row) & 1));
-            src += step;
+            for (int j = 0; j < kEach; ++j, src += step) copy16(copy_to(dst, m * kEach + j), src, policy);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kEach; ++j, src += step)
+              copy16(copy_to(dst, m * kEach + j), src, policy, (live >> (m * 16 + j * kRows + row0)) & 1);
           }
         }
       } else {
+        const unsigned char* const first = base - row0 * tok;
 #pragma unroll
         for (int j = 0; j < kCopies; ++j) {
           const int row = j * kRows + row0;
           const int64_t rid = __shfl_sync(~0u, id, row), rin = __shfl_sync(~0u, in_page, row);
           const bool on = (live >> row) & 1;
-          copy16(dst + swizzled<kRow>(row, chunk0), on ? base + (rid * page + rin * tok) * kSize : base, on);
+          copy16(copy_to(dst, j), on ? first + (rid * page + rin * tok) : first, policy, on);
         }
       }
     };
@@ -406,13 +429,13 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
           masks[slot] = live;
           if (live != mask) *a.status = HHR_ERR_BAD_INDEX;
         }
-        copy_rows(ring + slot * 2 * kTile, Kh, a.k_page, a.k_tok);
+        copy_rows(ring + slot * 2 * kTile, Kh, k_page, k_tok);
       }
       copy_commit();
     };
     const auto issue_v = [&](int slot) {
       if (ld_left > 0) {
-        copy_rows(ring + slot * 2 * kTile + kTile, Vh, a.v_page, a.v_tok);
+        copy_rows(ring + slot * 2 * kTile + kTile, Vh, v_page, v_tok);
         if (--ld_left > 0) {
           ld.next<kTokens>(a, units);
           find();
@@ -429,6 +452,8 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
 
     unsigned char* const my_q = smem + S::kQ + warp * S::kQWarp;
     const uint32_t q_smem = static_cast<uint32_t>(__cvta_generic_to_shared(my_q));
+    const uint32_t lane_k = turn<kRow>(lane & 15, lane >> 4);
+    const uint32_t lane_v = turn<kRow>((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
     int slot = 0;
     int64_t f = w0;
 
@@ -544,10 +569,15 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
 #pragma unroll
           for (int i = 0; i < kSub; ++i) {
             uint32_t r[4];
-            ldsm4(r, kt + swizzled<kRow>(i * 16 + (lane & 15), (S::kE4 ? k : 2 * k) + (lane >> 4)));
+            ldsm4(r, kt + chunk_at<kRow>(lane_k, S::kE4 ? k : 2 * k) + i * 16 * kRow);
             if constexpr (S::kE4) {
-              dot(i, k, {wide_lo(r[0]), wide_lo(r[1]), wide_hi(r[0]), wide_hi(r[1])});
-              dot(i, k + 1, {wide_lo(r[2]), wide_lo(r[3]), wide_hi(r[2]), wide_hi(r[3])});
+              uint32_t x[4], y[4];
+              widen(r[0], x[0], x[2]);
+              widen(r[1], x[1], x[3]);
+              widen(r[2], y[0], y[2]);
+              widen(r[3], y[1], y[3]);
+              dot(i, k, x);
+              dot(i, k + 1, y);
             } else {
               dot(i, k, r);
             }
@@ -626,13 +656,18 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
             uint32_t r[4];
             if constexpr (S::kE4) {
               // a transposed 2-byte element is columns 2 g and 2 g + 1 of a token: rows g and g + 8 of the product
-              ldsm4_trans(r, vt + swizzled<kRow>(i * 16 + (lane & 15), j + (lane >> 4)));
+              ldsm4_trans(r, vt + chunk_at<kRow>(lane_k, j) + i * 16 * kRow);
 #pragma unroll
               for (int e = 0; e < 4; ++e) r[e] = __byte_perm(r[e], 0, 0x3120);
-              add(j, {wide_lo(r[0]), wide_hi(r[0]), wide_lo(r[1]), wide_hi(r[1])});
-              add(j + 1, {wide_lo(r[2]), wide_hi(r[2]), wide_lo(r[3]), wide_hi(r[3])});
+              uint32_t x[4], y[4];
+              widen(r[0], x[0], x[1]);
+              widen(r[1], x[2], x[3]);
+              widen(r[2], y[0], y[1]);
+              widen(r[3], y[2], y[3]);
+              add(j, x);
+              add(j + 1, y);
             } else {
-              ldsm4_trans(r, vt + swizzled<kRow>(i * 16 + (lane & 7) + (lane >> 4) * 8, 2 * j + ((lane >> 3) & 1)));
+              ldsm4_trans(r, vt + chunk_at<kRow>(lane_v, 2 * j) + i * 16 * kRow);
               add(j, r);
             }
           }
@@ -692,7 +727,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
             }
             if (g == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[n][e] == -INFINITY ? -INFINITY : base[n][e], l[n][e]);
           }
-        if (lane == 0) s_open[2 * warp + last] = {x0, x1, to, seg.b, seg.u};
+        if (lane == 0) s_open[2 * warp + last] = {x0, x1, seg.b, seg.u};
       }
       if (f == w1) break;
       seg.at = seg.t.end - 1;
@@ -701,7 +736,8 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
   }
   __syncthreads();
 
-  // ---- open states, in the order of the tokens: those of one unit are joined
+  // ---- open states, in the order of the tokens: those of one unit are joined.  A unit's states lie over the rings of
+  // adjacent warps, but for that of a warp that went on to another unit.
   const auto finish = [&](size_t at, float4 y, float inv) {   // four columns
     if (a.out_f32) {
       *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
@@ -714,123 +750,205 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
       *reinterpret_cast<Pack<TQ, 4>*>(static_cast<TQ*>(a.out) + at) = p;
     }
   };
-  for (int i0 = 0, i1; i0 < 2 * kWarps; i0 = i1) {
-    i1 = i0 + 1;
-    const int64_t x0 = s_open[i0].x0, x1 = s_open[i0].x1;
-    if (x1 == 0) continue;
-    int states = 1;
-    uint32_t which = 1u << i0;
-    while (i1 < 2 * kWarps && (s_open[i1].x1 == 0 || s_open[i1].x0 == x0)) {
-      if (s_open[i1].x1) {
-        which |= 1u << i1;
-        ++states;
-      }
-      ++i1;
+  struct Shared {
+    size_t out_row;
+    int heads, c0, parts;
+  } shared[2];            // units shared with CTAs before (0) and behind (1)
+  shared[0].parts = shared[1].parts = 0;
+  {
+    int64_t x0 = 0, x1 = 0;
+    int b = 0, u = 0;
+    if (lane < 2 * kWarps) {
+      x0 = s_open[lane].x0;
+      x1 = s_open[lane].x1;
+      b = s_open[lane].b;
+      u = s_open[lane].u;
     }
-    const int b = s_open[i0].b, u = s_open[i0].u;
-    const int g_kv = u / a.chunks, first_head = (u - g_kv * a.chunks) * a.chunk;
-    const int heads = min(a.chunk, a.r - first_head);
-    const size_t out_row = static_cast<size_t>(b) * a.Hq + g_kv * a.r + first_head;
-    const bool inside = x0 >= f0 && x1 <= f1;
-    const int c0 = inside ? c : cta_of(x0);
-    float* const part = a.parts + static_cast<size_t>(2 * c + (c == c0)) * a.state;
-    for (int e = tid; e < heads * (D / 4); e += kThreads) {
-      const int h = e / (D / 4), d = e % (D / 4) * 4;
-      float top = -INFINITY, sum = 0;
-      for (uint32_t w = which; w; w &= w - 1) top = fmaxf(top, s_open[__ffs(w) - 1].at[h * (D + 4) + D]);
-      float4 y = make_float4(0, 0, 0, 0);
-      for (uint32_t w = which; w; w &= w - 1) {
-        const float* const row = s_open[__ffs(w) - 1].at + h * (D + 4);
-        const float2 ml = *reinterpret_cast<const float2*>(row + D);
-        const float4 x = *reinterpret_cast<const float4*>(row + d);
-        const float by = paged_weight(ml.x, top);
-        sum = fmaf(ml.y, by, sum);
-        y.x = fmaf(x.x, by, y.x);
-        y.y = fmaf(x.y, by, y.y);
-        y.z = fmaf(x.z, by, y.z);
-        y.w = fmaf(x.w, by, y.w);
-      }
-      if (inside) {
-        finish((out_row + h) * D + d, y, paged_inverse(sum, a.v_scale));
-        if (d == 0 && a.lse) a.lse[out_row + h] = paged_log_sum(top, sum);
-      } else {
-        *reinterpret_cast<float4*>(part + h * (D + 4) + d) = y;
-        if (d == 0) *reinterpret_cast<float2*>(part + h * (D + 4) + D) = make_float2(top, sum);
-      }
-    }
-    if (inside) continue;
-
-    // The last of the unit's CTAs to arrive joins their states from L2.
-    const int n_parts = cta_of(x1 - 1) - c0 + 1;
-    __syncthreads();
-    if (tid == 0) {
-      __threadfence();
-      const bool last = atomicAdd(a.counters + c0, 1u) == static_cast<uint32_t>(n_parts - 1);
-      if (last) a.counters[c0] = 0;
-      __threadfence();
-      s_last = last;
-    }
-    __syncthreads();
-    if (!s_last) continue;
-    float* const by = reinterpret_cast<float*>(smem + S::kQ);   // [8][n_parts]
-    float* const invs = by + 8 * kPagedMaxGrid;                 // [8]
-    float4* const sums = reinterpret_cast<float4*>(invs + 8);   // [kThreads]
-    const auto part_of = [&](int i) { return a.parts + static_cast<size_t>(2 * (c0 + i) + (i == 0)) * a.state; };
-    for (int h0 = 0; h0 < heads; h0 += 8) {
-      const int n_heads = min(8, heads - h0);
-      for (int h = warp; h < n_heads; h += kWarps) {
-        float top = -INFINITY, sum = 0;
-        for (int i = lane; i < n_parts; i += 32) top = fmaxf(top, __ldcg(part_of(i) + (h0 + h) * (D + 4) + D));
+    const uint32_t open = __ballot_sync(~0u, x1 != 0);
+    const uint32_t ahead = open & ((1u << lane) - 1);
+    const int64_t x0_ahead = __shfl_sync(~0u, x0, ahead ? 31 - __clz(ahead) : 0);
+    uint32_t heads_of = __ballot_sync(~0u, x1 != 0 && (!ahead || x0_ahead != x0));   // first states of their units
+    while (heads_of) {
+      const int i0 = __ffs(heads_of) - 1;
+      heads_of &= heads_of - 1;
+      const uint32_t mine = open & (heads_of ? (1u << (__ffs(heads_of) - 1)) - 1 : ~0u);
+      const int i1 = 31 - __clz(mine);
+      const int64_t y0 = __shfl_sync(~0u, x0, i0), y1 = __shfl_sync(~0u, x1, i0);
+      const int yb = __shfl_sync(~0u, b, i0), yu = __shfl_sync(~0u, u, i0);
+      const int g_kv = yu / a.chunks, first_head = (yu - g_kv * a.chunks) * a.chunk;
+      const int heads = min(a.chunk, a.r - first_head);
+      const size_t out_row = static_cast<size_t>(yb) * a.Hq + g_kv * a.r + first_head;
+      const bool inside = y0 >= f0 && y1 <= f1;
+      const int side = y0 >= f0;
+      float* const part = a.parts + static_cast<size_t>(2 * c + side) * a.state;
+      const int wa = i0 >> 1, wb = i1 >> 1;
+      const float* const last = (i1 & 1) ? reinterpret_cast<const float*>(smem + S::kRing + wb * S::kRingWarp)
+                                         : a.firsts + static_cast<size_t>(c * kWarps + wb) * a.state;
+      for (int e = tid; e < heads * (D / 4); e += kThreads) {
+        const int h = e / (D / 4), d = e % (D / 4) * 4;
+        float2 ml[kWarps];
+        float4 x[kWarps];
 #pragma unroll
-        for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
-        for (int i = lane; i < n_parts; i += 32) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_of(i) + (h0 + h) * (D + 4) + D));
-          const float x = paged_weight(ml.x, top);
-          by[h * n_parts + i] = x;
-          sum = fmaf(ml.y, x, sum);
+        for (int w = 0; w < kWarps; ++w) {
+          ml[w] = make_float2(-INFINITY, 0);
+          x[w] = make_float4(0, 0, 0, 0);
+          if (w >= wa && w < wb) {
+            const float* const row = reinterpret_cast<const float*>(smem + S::kRing + w * S::kRingWarp) + h * (D + 4);
+            ml[w] = *reinterpret_cast<const float2*>(row + D);
+            x[w] = *reinterpret_cast<const float4*>(row + d);
+          }
         }
+        float2 ml_last = *reinterpret_cast<const float2*>(last + h * (D + 4) + D);
+        float4 y = *reinterpret_cast<const float4*>(last + h * (D + 4) + d);
+        float top = ml_last.x;
 #pragma unroll
-        for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(~0u, sum, w);
-        if (lane == 0) {
-          invs[h] = paged_inverse(sum, a.v_scale);
-          if (a.lse) a.lse[out_row + h0 + h] = paged_log_sum(top, sum);
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w].x);
+        float by = paged_weight(ml_last.x, top);
+        float sum = ml_last.y * by;
+        y = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < wa || w >= wb) continue;
+          by = paged_weight(ml[w].x, top);
+          sum = fmaf(ml[w].y, by, sum);
+          y.x = fmaf(x[w].x, by, y.x);
+          y.y = fmaf(x[w].y, by, y.y);
+          y.z = fmaf(x[w].z, by, y.z);
+          y.w = fmaf(x[w].w, by, y.w);
+        }
+        if (inside) {
+          finish((out_row + h) * D + d, y, paged_inverse(sum, a.v_scale));
+          if (d == 0 && a.lse) a.lse[out_row + h] = paged_log_sum(top, sum);
+        } else {
+          *reinterpret_cast<float4*>(part + h * (D + 4) + d) = y;
+          if (d == 0) *reinterpret_cast<float2*>(part + h * (D + 4) + D) = make_float2(top, sum);
         }
       }
-      __syncthreads();
-      const int items = n_heads * (D / 4);                 // 4 columns each
-      const int splits = max(1, kThreads / items);         // parts are dealt out where there are few items
+      if (!inside) {
+        const int c0 = side ? c : cta_of(y0);
+        const Shared one = {out_row, heads, c0, cta_of(y1 - 1) - c0 + 1};
+        if (side)
+          shared[1] = one;
+        else
+          shared[0] = one;
+      }
+    }
+  }
+  if (shared[0].parts || shared[1].parts) {
+    // The last of a unit's CTAs to arrive joins their states from L2.  (The barrier and the acquire-release addition
+    // order every thread's state before the addition and the other CTAs' states behind it.)
+    __syncthreads();
+    if (lane == 0 && warp < 2) {
+      const Shared& one = warp ? shared[1] : shared[0];
+      int last = 0;
+      if (one.parts) {
+        uint32_t* const count = a.counters + one.c0;
+        uint32_t old;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(count) : "memory");
+        last = old == static_cast<uint32_t>(one.parts - 1);
+        if (last) *count = 0;
+      }
+      s_last[warp] = last;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      if (!s_last[side]) continue;
+      const Shared one = shared[side];
+      float4* const sums = reinterpret_cast<float4*>(smem + S::kQ);    // [kThreads]
+      float2* const mls = reinterpret_cast<float2*>(sums + kThreads);  // [kThreads]
+      const int items = one.heads * (D / 4);                // 4 columns each
+      const int splits = max(1, kThreads / items);          // parts are dealt out where there are few items
       for (int e0 = 0; e0 < items; e0 += kThreads) {
         const int e = splits > 1 ? tid % items : e0 + tid, sp = splits > 1 ? tid / items : 0;
         const int h = e / (D / 4), d = e % (D / 4) * 4;
+        float top = -INFINITY, sum = 0;
         float4 y = make_float4(0, 0, 0, 0);
         if (e < items && sp < splits) {
-#pragma unroll 8
-          for (int i = sp; i < n_parts; i += splits) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(part_of(i) + (h0 + h) * (D + 4) + d));
-            const float k = by[h * n_parts + i];
-            y.x = fmaf(x.x, k, y.x);
-            y.y = fmaf(x.y, k, y.y);
-            y.z = fmaf(x.z, k, y.z);
-            y.w = fmaf(x.w, k, y.w);
+          constexpr int kBatch = 8;
+          for (int i0 = sp; i0 < one.parts; i0 += splits * kBatch) {
+            float2 ml[kBatch];
+            float4 x[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const int i = i0 + k * splits;
+              ml[k] = make_float2(-INFINITY, 0);
+              x[k] = make_float4(0, 0, 0, 0);
+              if (i < one.parts) {
+                const float* const row = a.parts + static_cast<size_t>(2 * (one.c0 + i) + (i == 0)) * a.state + h * (D + 4);
+                ml[k] = __ldcg(reinterpret_cast<const float2*>(row + D));
+                x[k] = __ldcg(reinterpret_cast<const float4*>(row + d));
+              }
+            }
+            float next = top;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) next = fmaxf(next, ml[k].x);
+            float by = paged_weight(top, next);
+            sum *= by;
+            y = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
+            top = next;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              by = paged_weight(ml[k].x, top);
+              sum = fmaf(ml[k].y, by, sum);
+              y.x = fmaf(x[k].x, by, y.x);
+              y.y = fmaf(x[k].y, by, y.y);
+              y.z = fmaf(x[k].z, by, y.z);
+              y.w = fmaf(x[k].w, by, y.w);
+            }
           }
         }
         if (splits > 1) {
           sums[tid] = y;
+          mls[tid] = make_float2(top, sum);
           __syncthreads();
-          if (tid < items)
+          if (tid < items) {
+            float next = top;
+            for (int i = 1; i < splits; ++i) next = fmaxf(next, mls[i * items + tid].x);
+            float by = paged_weight(top, next);
+            sum *= by;
+            y = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
+            top = next;
             for (int i = 1; i < splits; ++i) {
               const float4 x = sums[i * items + tid];
-              y.x += x.x;
-              y.y += x.y;
-              y.z += x.z;
-              y.w += x.w;
+              const float2 ml = mls[i * items + tid];
+              by = paged_weight(ml.x, top);
+              sum = fmaf(ml.y, by, sum);
+              y.x = fmaf(x.x, by, y.x);
+              y.y = fmaf(x.y, by, y.y);
+              y.z = fmaf(x.z, by, y.z);
+              y.w = fmaf(x.w, by, y.w);
             }
+          }
+          __syncthreads();
         }
-        if (e < items && sp == 0) finish((out_row + h0 + h) * D + d, y, invs[h]);
+        if (e < items && sp == 0) {
+          finish((one.out_row + h) * D + d, y, paged_inverse(sum, a.v_scale));
+          if (d == 0 && a.lse) a.lse[one.out_row + h] = paged_log_sum(top, sum);
+        }
       }
-      __syncthreads();
     }
   }
+
+  // Rows of sequences without tokens, and lengths out of range.
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const int len = a.lens[b];
+    if (len < 0 || len > a.table_cols * a.page) {
+      if (tid == 0) *a.status = HHR_ERR_BAD_INDEX;
+    } else if (len > 0) {
+      continue;
+    }
+    const size_t row = static_cast<size_t>(b) * a.Hq;
+    for (int e = tid; e < a.Hq * D; e += kThreads) {
+      if (a.out_f32)
+        static_cast<float*>(a.out)[row * D + e] = 0.0f;
+      else
+        static_cast<TQ*>(a.out)[row * D + e] = from_f32<TQ>(0.0f);
+    }
+    if (a.lse)
+      for (int h = tid; h < a.Hq; h += kThreads) a.lse[row + h] = -INFINITY;
+  }
+
 }
 
 // Launches the variant for D and the heads of a unit.
