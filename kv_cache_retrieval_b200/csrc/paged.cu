@@ -25,7 +25,7 @@ extern "C" {
 size_t hhr_paged_workspace_size(const hhr_paged* cache) {
   if (check_paged(cache) != HHR_OK) return 0;
   const size_t state = paged_state(unit_heads(*cache), cache->d);
-  return align_up(kPagedParts + (2 + 8) * kPagedMaxGrid * state * sizeof(float), 256);
+  return align_up(kPagedParts + (2 + kPagedMaxWarps) * kPagedMaxGrid * state * sizeof(float), 256);
 }
 
 int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64_t q_seq,
@@ -46,6 +46,7 @@ int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64
       !aligned_to(lens, 4) || !aligned_to(lse, 4))
     return HHR_ERR_INVALID_ARG;
   if (B > 1 && (q_seq < 0 || q_seq % 8 != 0)) return HHR_ERR_INVALID_ARG;
+  const int size = type_size(c.kv_type);
   PagedArgs a;
   std::memset(&a, 0, sizeof a);
   a.q = q;
@@ -60,12 +61,12 @@ int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64
   a.counters = reinterpret_cast<uint32_t*>(ws + kPagedCounters);
   a.parts = reinterpret_cast<float*>(ws + kPagedParts);
   a.q_seq = q_seq;
-  a.k_page = c.k_page;
-  a.k_head = c.k_head;
-  a.k_tok = c.k_tok;
-  a.v_page = c.v_page;
-  a.v_head = c.v_head;
-  a.v_tok = c.v_tok;
+  a.k_page = c.k_page * size;
+  a.k_head = c.k_head * size;
+  a.k_tok = c.k_tok * size;
+  a.v_page = c.v_page * size;
+  a.v_head = c.v_head * size;
+  a.v_tok = c.v_tok * size;
   a.scale_log2 = scale * c.k_scale * 1.4426950408889634f;
   a.v_scale = c.v_scale;
   a.B = B;
@@ -84,7 +85,7 @@ int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64
   a.firsts = a.parts + static_cast<size_t>(2 * kPagedMaxGrid) * a.state;
   while ((int64_t{1} << a.page_shift) < c.page) ++a.page_shift;
   a.page_magic = static_cast<uint32_t>((((uint64_t{1} << a.page_shift) - c.page) << 32) / c.page + 1);
-  a.min_tiles = 4;
+  a.min_tiles = 2;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return HHR_ERR_CUDA;

@@ -38,6 +38,7 @@
 namespace hhr {
 
 constexpr int kPagedMaxGrid = 160;   // CTAs that take part in a call (one per SM)
+constexpr int kPagedMaxWarps = 16;   // warps of a CTA
 
 struct PagedArgs {
   const void* q;
@@ -50,8 +51,9 @@ struct PagedArgs {
   uint32_t* status;
   uint32_t* counters;          // [kPagedMaxGrid]: states that arrived for the unit a CTA began
   float* parts;                // [kPagedMaxGrid][2]: joined states of a CTA's first and last unit
-  float* firsts;               // [kPagedMaxGrid][8]: states of the units that a warp ends and did not begin
-  int64_t q_seq, k_page, k_head, k_tok, v_page, v_head, v_tok;
+  float* firsts;               // [kPagedMaxGrid][kPagedMaxWarps]: states of the units that a warp ends and did not begin
+  int64_t q_seq;                                              // elements
+  int64_t k_page, k_head, k_tok, v_page, v_head, v_tok;       // bytes
   float scale_log2, v_scale;
   int B, Hq, Hkv, page, n_pages, table_cols, table_stride, window, out_f32;
   int r, chunk, chunks;        // query heads of a KV head, of a unit (at most 8 NT), and units of a KV head
@@ -76,19 +78,20 @@ struct PagedShape {
   static constexpr int kHeads = 8 * NT;
   // registers hold the query fragments unless the sums leave no room: then each warp reads them from shared memory
   static constexpr bool kQRegs = D / 16 * NT * 2 <= 48;
-  static constexpr int kWarps = kRow > 256 || !kQRegs ? 4 : 8;
+  // More warps hide more latency where their registers allow it.
+  static constexpr int kWarps = D * NT <= 128 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kDepth = std::min(8, 196608 / (kWarps * 2 * kTile));
+  static constexpr int kDepth = std::max(1, 131072 / (kWarps * 2 * kTile));
   // shared memory
   static constexpr int kRing = 0;
-  static constexpr int kRingWarp = kDepth * 2 * kTile;            // of a warp; in the end it holds the warp's last state
+  // of a warp; in the end it holds the warp's last state
+  static constexpr int kRingWarp = std::max(kDepth * 2 * kTile, (kHeads * (D + 4) * 4 + 127) / 128 * 128);
   static constexpr int kQ = kRing + kWarps * kRingWarp;
   static constexpr int kQWarp = kQRegs ? 0 : kHeads * D * 2;
-  static constexpr int kJoin = kThreads * 24;                     // the threads' sums, maxima and weight sums in the join
-  static constexpr int kMasks = kQ + std::max(kWarps * kQWarp, kJoin);
+  static constexpr int kSlots = kWarps * kRingWarp / (kHeads * (D + 4) * 4);   // states that the rings hold in the join
+  static constexpr int kMasks = kQ + kWarps * kQWarp;
   static constexpr int kSmem = kMasks + kWarps * kDepth * 4;
   static_assert(kSmem <= 226 * 1024, "shared memory of a CTA");
-  static_assert(kHeads * (D + 4) * 4 <= kRingWarp, "a warp's state lies in its ring");
 };
 
 // Tiles of a sequence: [first, end).
@@ -236,6 +239,69 @@ __device__ __forceinline__ float paged_log_sum(float top, float sum) {
   return sum == 0 ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
 }
 
+// A join of n states: the i-th at base + i * stride, the last at `last` unless that is null; into the state `to` (none of
+// these), or, if that is null, into the output's rows from out_row on.
+struct Join {
+  const float* base;
+  const float* last;
+  float* to;
+  size_t out_row;
+  int64_t x0, x1;       // the unit's tiles
+  int stride, n, heads;
+};
+
+// All threads of a CTA do `count` joins side by side, a thread four columns of a head at a time.  One copy of this code
+// serves all joins: it is fetched cold.
+template <typename TQ, int D, int kThreads>
+__device__ __noinline__ void join_states(const PagedArgs& a, const Join* joins, int count) {
+  const int most = a.chunk * (D / 4);
+#pragma unroll 1
+  for (int e = threadIdx.x; e < count * most; e += kThreads) {
+    const int k = e / most, item = e - k * most, h = item / (D / 4), d = item % (D / 4) * 4;
+    const Join& j = joins[k];
+    const int n = j.n;
+    if (h >= j.heads) continue;
+    const float* const base = j.base + h * (D + 4);
+    const float* const last = (j.last ? j.last : j.base + (n - 1) * j.stride) + h * (D + 4);
+    const int stride = j.stride;
+    float top = last[D];
+#pragma unroll 4
+    for (int i = 0; i < n - 1; ++i) top = fmaxf(top, base[i * stride + D]);
+    float sum = 0;
+    float4 y = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float* const row = i < n - 1 ? base + i * stride : last;
+      const float2 ml = *reinterpret_cast<const float2*>(row + D);
+      const float4 x = *reinterpret_cast<const float4*>(row + d);
+      const float by = paged_weight(ml.x, top);
+      sum = fmaf(ml.y, by, sum);
+      y.x = fmaf(x.x, by, y.x);
+      y.y = fmaf(x.y, by, y.y);
+      y.z = fmaf(x.z, by, y.z);
+      y.w = fmaf(x.w, by, y.w);
+    }
+    if (j.to) {
+      *reinterpret_cast<float4*>(j.to + h * (D + 4) + d) = y;
+      if (d == 0) *reinterpret_cast<float2*>(j.to + h * (D + 4) + D) = make_float2(top, sum);
+      continue;
+    }
+    const float inv = paged_inverse(sum, a.v_scale);
+    const size_t at = (j.out_row + h) * D + d;
+    if (a.out_f32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+    } else {
+      Pack<TQ, 4> p;
+      p.v[0] = from_f32<TQ>(y.x * inv);
+      p.v[1] = from_f32<TQ>(y.y * inv);
+      p.v[2] = from_f32<TQ>(y.z * inv);
+      p.v[3] = from_f32<TQ>(y.w * inv);
+      *reinterpret_cast<Pack<TQ, 4>*>(static_cast<TQ*>(a.out) + at) = p;
+    }
+    if (d == 0 && a.lse) a.lse[j.out_row + h] = paged_log_sum(top, sum);
+  }
+}
+
 template <typename TQ, typename TC, int D, int NT>
 __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_kernel(const PagedArgs a) {
   using S = PagedShape<TQ, TC, D, NT>;
@@ -248,7 +314,10 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
   constexpr float kLift = std::is_same<TM, __half>::value ? 14.0f : 0.0f;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t s_scan[kWarps], s_before[kThreads];
-  __shared__ int s_seqs[kWarps], s_last[2];
+  __shared__ Join s_join[kWarps + 1];
+  __shared__ int s_joins, s_side[2];                  // joins; those of the units shared with the CTAs before and behind
+  __shared__ int s_last[2], s_first[2];               // of these: states if this CTA joins them, first CTA
+  __shared__ int s_seqs[kWarps];
   __shared__ OpenState s_open[2 * kWarps];   // of a warp: of the unit it ends, of the unit it leaves unfinished
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
@@ -315,14 +384,16 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
   int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(int64_t{1}, total / (kWarps * a.min_tiles))));
   if (G < gridDim.x && static_cast<int64_t>(n_seqs) * units <= G) G -= G % (n_seqs * units);
   const int c = blockIdx.x;
-  // warp i of the G kWarps takes [first_of(i), first_of(i + 1)) (the host bounds total * G * kWarps)
-  const uint32_t n_warps = G * kWarps;
-  const auto first_of = [&](int i) { return static_cast<int64_t>(static_cast<uint64_t>(total) * i / n_warps); };
+  // Warp i of them takes [first_of(i), first_of(i + 1)), a tile at least (the host bounds total * n_warps).
+  const uint32_t n_warps = static_cast<uint32_t>(max(int64_t{1}, min(static_cast<int64_t>(G) * kWarps, total)));
+  const auto first_of = [&](int i) {
+    return static_cast<int64_t>(static_cast<uint64_t>(total) * min(static_cast<uint32_t>(i), n_warps) / n_warps);
+  };
   const auto cta_of = [&](int64_t x) {   // the CTA whose range holds x
     return static_cast<int>((static_cast<uint64_t>(x + 1) * n_warps - 1) / static_cast<uint64_t>(total)) / kWarps;
   };
   const int64_t f0 = first_of(c * kWarps), f1 = first_of((c + 1) * kWarps);
-  const int64_t w0 = first_of(c * kWarps + warp), w1 = c < G ? first_of(c * kWarps + warp + 1) : w0;
+  const int64_t w0 = first_of(c * kWarps + warp), w1 = first_of(c * kWarps + warp + 1);
 
   if (w0 < w1) {
     // ---- where w0 lies: the last run that begins at or before it, then the sequence
@@ -355,16 +426,13 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
     unsigned char* const my_ring = smem + S::kRing + warp * S::kRingWarp;
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(my_ring));
     uint32_t* const masks = reinterpret_cast<uint32_t*>(smem + S::kMasks) + warp * kDepth;
-    constexpr int kSize = static_cast<int>(sizeof(TC));
     constexpr int kChunks = kRow / 16;               // 16-byte chunks of a row
     constexpr int kRows = kChunks >= 32 ? 1 : 32 / kChunks;   // rows of a warp's copy
     constexpr int kCopies = kTokens / kRows;
     const int row0 = lane / kChunks, chunk0 = lane % kChunks;
     const bool whole = (a.page & 15) == 0;           // 16 rows do not cross pages
-    const int64_t k_page = a.k_page * kSize, k_tok = a.k_tok * kSize, k_head = a.k_head * kSize;   // bytes
-    const int64_t v_page = a.v_page * kSize, v_tok = a.v_tok * kSize, v_head = a.v_head * kSize;
-    const unsigned char* const Kb = static_cast<const unsigned char*>(a.K) + chunk0 * 16 + row0 * k_tok;
-    const unsigned char* const Vb = static_cast<const unsigned char*>(a.V) + chunk0 * 16 + row0 * v_tok;
+    const unsigned char* const Kb = static_cast<const unsigned char*>(a.K) + chunk0 * 16 + row0 * a.k_tok;
+    const unsigned char* const Vb = static_cast<const unsigned char*>(a.V) + chunk0 * 16 + row0 * a.v_tok;
     TileCursor ld = seg;
     int64_t ld_left = w1 - w0;   // tiles that have not been asked for
     const unsigned char *Kh = Kb, *Vh = Vb;   // of the tile's KV head
@@ -384,8 +452,8 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
       if (ask) id = a.table[static_cast<int64_t>(ld.b) * a.table_stride + p];
       mask = rows & kAll;
       const int kv = a.chunks == 1 ? ld.u : ld.u / a.chunks;
-      Kh = Kb + kv * k_head;
-      Vh = Vb + kv * v_head;
+      Kh = Kb + kv * a.k_head;
+      Vh = Vb + kv * a.v_head;
     };
     const uint64_t policy = read_once();
     const uint32_t lane_c = turn<kRow>(row0, chunk0);
@@ -429,13 +497,13 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
           masks[slot] = live;
           if (live != mask) *a.status = HHR_ERR_BAD_INDEX;
         }
-        copy_rows(ring + slot * 2 * kTile, Kh, k_page, k_tok);
+        copy_rows(ring + slot * 2 * kTile, Kh, a.k_page, a.k_tok);
       }
       copy_commit();
     };
     const auto issue_v = [&](int slot) {
       if (ld_left > 0) {
-        copy_rows(ring + slot * 2 * kTile + kTile, Vh, v_page, v_tok);
+        copy_rows(ring + slot * 2 * kTile + kTile, Vh, a.v_page, a.v_tok);
         if (--ld_left > 0) {
           ld.next<kTokens>(a, units);
           find();
@@ -736,196 +804,106 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
   }
   __syncthreads();
 
-  // ---- open states, in the order of the tokens: those of one unit are joined.  A unit's states lie over the rings of
-  // adjacent warps, but for that of a warp that went on to another unit.
-  const auto finish = [&](size_t at, float4 y, float inv) {   // four columns
-    if (a.out_f32) {
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
-    } else {
-      Pack<TQ, 4> p;
-      p.v[0] = from_f32<TQ>(y.x * inv);
-      p.v[1] = from_f32<TQ>(y.y * inv);
-      p.v[2] = from_f32<TQ>(y.z * inv);
-      p.v[3] = from_f32<TQ>(y.w * inv);
-      *reinterpret_cast<Pack<TQ, 4>*>(static_cast<TQ*>(a.out) + at) = p;
-    }
-  };
-  struct Shared {
-    size_t out_row;
-    int heads, c0, parts;
-  } shared[2];            // units shared with CTAs before (0) and behind (1)
-  shared[0].parts = shared[1].parts = 0;
-  {
+  // ---- open states, in the order of the tokens: those of one unit are joined.  They lie over the rings of adjacent
+  // warps, but for that of a warp that went on to another unit.
+  float* const rings = reinterpret_cast<float*>(smem + S::kRing);
+  if (warp == 0) {   // a lane per state lists the joins
     int64_t x0 = 0, x1 = 0;
-    int b = 0, u = 0;
     if (lane < 2 * kWarps) {
       x0 = s_open[lane].x0;
       x1 = s_open[lane].x1;
-      b = s_open[lane].b;
-      u = s_open[lane].u;
     }
     const uint32_t open = __ballot_sync(~0u, x1 != 0);
     const uint32_t ahead = open & ((1u << lane) - 1);
     const int64_t x0_ahead = __shfl_sync(~0u, x0, ahead ? 31 - __clz(ahead) : 0);
-    uint32_t heads_of = __ballot_sync(~0u, x1 != 0 && (!ahead || x0_ahead != x0));   // first states of their units
-    while (heads_of) {
-      const int i0 = __ffs(heads_of) - 1;
-      heads_of &= heads_of - 1;
-      const uint32_t mine = open & (heads_of ? (1u << (__ffs(heads_of) - 1)) - 1 : ~0u);
-      const int i1 = 31 - __clz(mine);
-      const int64_t y0 = __shfl_sync(~0u, x0, i0), y1 = __shfl_sync(~0u, x1, i0);
-      const int yb = __shfl_sync(~0u, b, i0), yu = __shfl_sync(~0u, u, i0);
-      const int g_kv = yu / a.chunks, first_head = (yu - g_kv * a.chunks) * a.chunk;
-      const int heads = min(a.chunk, a.r - first_head);
-      const size_t out_row = static_cast<size_t>(yb) * a.Hq + g_kv * a.r + first_head;
-      const bool inside = y0 >= f0 && y1 <= f1;
-      const int side = y0 >= f0;
-      float* const part = a.parts + static_cast<size_t>(2 * c + side) * a.state;
-      const int wa = i0 >> 1, wb = i1 >> 1;
-      const float* const last = (i1 & 1) ? reinterpret_cast<const float*>(smem + S::kRing + wb * S::kRingWarp)
-                                         : a.firsts + static_cast<size_t>(c * kWarps + wb) * a.state;
-      for (int e = tid; e < heads * (D / 4); e += kThreads) {
-        const int h = e / (D / 4), d = e % (D / 4) * 4;
-        float2 ml[kWarps];
-        float4 x[kWarps];
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          ml[w] = make_float2(-INFINITY, 0);
-          x[w] = make_float4(0, 0, 0, 0);
-          if (w >= wa && w < wb) {
-            const float* const row = reinterpret_cast<const float*>(smem + S::kRing + w * S::kRingWarp) + h * (D + 4);
-            ml[w] = *reinterpret_cast<const float2*>(row + D);
-            x[w] = *reinterpret_cast<const float4*>(row + d);
-          }
-        }
-        float2 ml_last = *reinterpret_cast<const float2*>(last + h * (D + 4) + D);
-        float4 y = *reinterpret_cast<const float4*>(last + h * (D + 4) + d);
-        float top = ml_last.x;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w].x);
-        float by = paged_weight(ml_last.x, top);
-        float sum = ml_last.y * by;
-        y = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          if (w < wa || w >= wb) continue;
-          by = paged_weight(ml[w].x, top);
-          sum = fmaf(ml[w].y, by, sum);
-          y.x = fmaf(x[w].x, by, y.x);
-          y.y = fmaf(x[w].y, by, y.y);
-          y.z = fmaf(x[w].z, by, y.z);
-          y.w = fmaf(x[w].w, by, y.w);
-        }
-        if (inside) {
-          finish((out_row + h) * D + d, y, paged_inverse(sum, a.v_scale));
-          if (d == 0 && a.lse) a.lse[out_row + h] = paged_log_sum(top, sum);
-        } else {
-          *reinterpret_cast<float4*>(part + h * (D + 4) + d) = y;
-          if (d == 0) *reinterpret_cast<float2*>(part + h * (D + 4) + D) = make_float2(top, sum);
-        }
-      }
-      if (!inside) {
-        const int c0 = side ? c : cta_of(y0);
-        const Shared one = {out_row, heads, c0, cta_of(y1 - 1) - c0 + 1};
-        if (side)
-          shared[1] = one;
-        else
-          shared[0] = one;
-      }
+    const bool begins = x1 != 0 && (!ahead || x0_ahead != x0);   // the first state of its unit
+    const uint32_t all = __ballot_sync(~0u, begins);
+    if (lane == 0) {
+      s_joins = __popc(all);
+      s_side[0] = s_side[1] = -1;
+    }
+    __syncwarp();
+    if (begins) {
+      const int k = __popc(all & ((1u << lane) - 1));
+      const uint32_t behind = all & ~((2u << lane) - 1);
+      const uint32_t upto = open & (behind ? (1u << (__ffs(behind) - 1)) - 1 : ~0u);
+      const int i1 = 31 - __clz(upto), wa = lane >> 1, wb = i1 >> 1;
+      const int b = s_open[lane].b, u = s_open[lane].u;
+      const int g_kv = u / a.chunks, first_head = (u - g_kv * a.chunks) * a.chunk;
+      const bool inside = x0 >= f0 && x1 <= f1;
+      const int side = x0 >= f0;
+      Join& j = s_join[k];
+      j.base = rings + wa * (S::kRingWarp / 4);
+      j.last = (i1 & 1) ? nullptr : a.firsts + static_cast<size_t>(c * kWarps + wb) * a.state;
+      j.to = inside ? nullptr : a.parts + static_cast<size_t>(2 * c + side) * a.state;
+      j.out_row = static_cast<size_t>(b) * a.Hq + g_kv * a.r + first_head;
+      j.x0 = x0;
+      j.x1 = x1;
+      j.stride = S::kRingWarp / 4;
+      j.n = wb - wa + 1;
+      j.heads = min(a.chunk, a.r - first_head);
+      if (!inside) s_side[side] = k;
     }
   }
-  if (shared[0].parts || shared[1].parts) {
-    // The last of a unit's CTAs to arrive joins their states from L2.  (The barrier and the acquire-release addition
-    // order every thread's state before the addition and the other CTAs' states behind it.)
+  __syncthreads();
+  join_states<TQ, D, kThreads>(a, s_join, s_joins);
+
+  if (s_side[0] >= 0 || s_side[1] >= 0) {
+    // Units shared with CTAs before (0) and behind (1).  The last of a unit's CTAs to arrive joins their states from L2.
+    // (The barrier and the acquire-release addition order every thread's state before the addition and the other CTAs'
+    // states behind it.)
     __syncthreads();
     if (lane == 0 && warp < 2) {
-      const Shared& one = warp ? shared[1] : shared[0];
-      int last = 0;
-      if (one.parts) {
-        uint32_t* const count = a.counters + one.c0;
+      int n = 0, c0 = 0;
+      if (s_side[warp] >= 0) {
+        const Join& j = s_join[s_side[warp]];
+        c0 = cta_of(j.x0);
+        n = cta_of(j.x1 - 1) - c0 + 1;
+        uint32_t* const count = a.counters + c0;
         uint32_t old;
         asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(count) : "memory");
-        last = old == static_cast<uint32_t>(one.parts - 1);
-        if (last) *count = 0;
+        if (old == static_cast<uint32_t>(n - 1))
+          *count = 0;
+        else
+          n = 0;
       }
-      s_last[warp] = last;
+      s_last[warp] = n;
+      s_first[warp] = c0;
     }
     __syncthreads();
-#pragma unroll
+#pragma unroll 1
     for (int side = 0; side < 2; ++side) {
-      if (!s_last[side]) continue;
-      const Shared one = shared[side];
-      float4* const sums = reinterpret_cast<float4*>(smem + S::kQ);    // [kThreads]
-      float2* const mls = reinterpret_cast<float2*>(sums + kThreads);  // [kThreads]
-      const int items = one.heads * (D / 4);                // 4 columns each
-      const int splits = max(1, kThreads / items);          // parts are dealt out where there are few items
-      for (int e0 = 0; e0 < items; e0 += kThreads) {
-        const int e = splits > 1 ? tid % items : e0 + tid, sp = splits > 1 ? tid / items : 0;
-        const int h = e / (D / 4), d = e % (D / 4) * 4;
-        float top = -INFINITY, sum = 0;
-        float4 y = make_float4(0, 0, 0, 0);
-        if (e < items && sp < splits) {
-          constexpr int kBatch = 8;
-          for (int i0 = sp; i0 < one.parts; i0 += splits * kBatch) {
-            float2 ml[kBatch];
-            float4 x[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              const int i = i0 + k * splits;
-              ml[k] = make_float2(-INFINITY, 0);
-              x[k] = make_float4(0, 0, 0, 0);
-              if (i < one.parts) {
-                const float* const row = a.parts + static_cast<size_t>(2 * (one.c0 + i) + (i == 0)) * a.state + h * (D + 4);
-                ml[k] = __ldcg(reinterpret_cast<const float2*>(row + D));
-                x[k] = __ldcg(reinterpret_cast<const float4*>(row + d));
-              }
-            }
-            float next = top;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) next = fmaxf(next, ml[k].x);
-            float by = paged_weight(top, next);
-            sum *= by;
-            y = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
-            top = next;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              by = paged_weight(ml[k].x, top);
-              sum = fmaf(ml[k].y, by, sum);
-              y.x = fmaf(x[k].x, by, y.x);
-              y.y = fmaf(x[k].y, by, y.y);
-              y.z = fmaf(x[k].z, by, y.z);
-              y.w = fmaf(x[k].w, by, y.w);
-            }
-          }
+      const int n = s_last[side], c0 = s_first[side];
+      if (n == 0) continue;
+      Join& j = s_join[s_side[side]];
+      const int words = j.heads * (D + 4);                  // floats of a state
+      // as many at a time as the rings hold behind two slots, which in turn have what was joined before
+      int kept = -1;
+#pragma unroll 1
+      for (int done = 0; done < n;) {
+        const int now = min(n - done, S::kSlots - 2);
+#pragma unroll 1
+        for (int i = warp; i < now; i += kWarps) {
+          const float* const from = a.parts + static_cast<size_t>(2 * (c0 + done + i) + (done + i == 0)) * a.state;
+          const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(rings + (2 + i) * words));
+          for (int k = lane * 4; k < words; k += 128)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k * 4), "l"(from + k) : "memory");
         }
-        if (splits > 1) {
-          sums[tid] = y;
-          mls[tid] = make_float2(top, sum);
-          __syncthreads();
-          if (tid < items) {
-            float next = top;
-            for (int i = 1; i < splits; ++i) next = fmaxf(next, mls[i * items + tid].x);
-            float by = paged_weight(top, next);
-            sum *= by;
-            y = make_float4(y.x * by, y.y * by, y.z * by, y.w * by);
-            top = next;
-            for (int i = 1; i < splits; ++i) {
-              const float4 x = sums[i * items + tid];
-              const float2 ml = mls[i * items + tid];
-              by = paged_weight(ml.x, top);
-              sum = fmaf(ml.y, by, sum);
-              y.x = fmaf(x.x, by, y.x);
-              y.y = fmaf(x.y, by, y.y);
-              y.z = fmaf(x.z, by, y.z);
-              y.w = fmaf(x.w, by, y.w);
-            }
-          }
-          __syncthreads();
+        copy_commit();
+        copy_wait<0>();
+        done += now;
+        __syncthreads();
+        if (tid == 0) {
+          j.base = rings + 2 * words;
+          j.last = kept < 0 ? nullptr : rings + kept * words;
+          j.to = done < n ? rings + (kept != 0 ? 0 : words) : nullptr;
+          j.stride = words;
+          j.n = now + (kept >= 0);
         }
-        if (e < items && sp == 0) {
-          finish((one.out_row + h) * D + d, y, paged_inverse(sum, a.v_scale));
-          if (d == 0 && a.lse) a.lse[one.out_row + h] = paged_log_sum(top, sum);
-        }
+        kept = kept != 0 ? 0 : 1;
+        __syncthreads();
+        join_states<TQ, D, kThreads>(a, &j, 1);
+        __syncthreads();
       }
     }
   }
