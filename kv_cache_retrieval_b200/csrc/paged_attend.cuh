@@ -88,7 +88,6 @@ struct PagedShape {
   static constexpr int kRingWarp = std::max(kDepth * 2 * kTile, (kHeads * (D + 4) * 4 + 127) / 128 * 128);
   static constexpr int kQ = kRing + kWarps * kRingWarp;
   static constexpr int kQWarp = kQRegs ? 0 : kHeads * D * 2;
-  static constexpr int kSlots = kWarps * kRingWarp / (kHeads * (D + 4) * 4);   // states that the rings hold in the join
   static constexpr int kMasks = kQ + kWarps * kQWarp;
   static constexpr int kSmem = kMasks + kWarps * kDepth * 4;
   static_assert(kSmem <= 226 * 1024, "shared memory of a CTA");
@@ -262,24 +261,41 @@ __device__ __noinline__ void join_states(const PagedArgs& a, const Join* joins, 
     const int n = j.n;
     if (h >= j.heads) continue;
     const float* const base = j.base + h * (D + 4);
-    const float* const last = (j.last ? j.last : j.base + (n - 1) * j.stride) + h * (D + 4);
     const int stride = j.stride;
-    float top = last[D];
-#pragma unroll 4
-    for (int i = 0; i < n - 1; ++i) top = fmaxf(top, base[i * stride + D]);
-    float sum = 0;
+    const float* const last = j.last ? j.last + h * (D + 4) : base + (n - 1) * stride;
+    float top = -INFINITY, sum = 0;
     float4 y = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float* const row = i < n - 1 ? base + i * stride : last;
-      const float2 ml = *reinterpret_cast<const float2*>(row + D);
-      const float4 x = *reinterpret_cast<const float4*>(row + d);
-      const float by = paged_weight(ml.x, top);
-      sum = fmaf(ml.y, by, sum);
-      y.x = fmaf(x.x, by, y.x);
-      y.y = fmaf(x.y, by, y.y);
-      y.z = fmaf(x.z, by, y.z);
-      y.w = fmaf(x.w, by, y.w);
+    constexpr int kBatch = 8;    // loads in flight: the states may lie in L2
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+      float2 ml[kBatch];
+      float4 x[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        ml[k] = make_float2(-INFINITY, 0);
+        x[k] = make_float4(0, 0, 0, 0);
+        if (i0 + k < n) {
+          const float* const row = i0 + k < n - 1 ? base + (i0 + k) * stride : last;
+          ml[k] = *reinterpret_cast<const float2*>(row + D);
+          x[k] = *reinterpret_cast<const float4*>(row + d);
+        }
+      }
+      float next = top;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) next = fmaxf(next, ml[k].x);
+      const float was = paged_weight(top, next);
+      sum *= was;
+      y = make_float4(y.x * was, y.y * was, y.z * was, y.w * was);
+      top = next;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float by = paged_weight(ml[k].x, top);
+        sum = fmaf(ml[k].y, by, sum);
+        y.x = fmaf(x[k].x, by, y.x);
+        y.y = fmaf(x[k].y, by, y.y);
+        y.z = fmaf(x[k].z, by, y.z);
+        y.w = fmaf(x[k].w, by, y.w);
+      }
     }
     if (j.to) {
       *reinterpret_cast<float4*>(j.to + h * (D + 4) + d) = y;
@@ -316,7 +332,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
   __shared__ int64_t s_scan[kWarps], s_before[kThreads];
   __shared__ Join s_join[kWarps + 1];
   __shared__ int s_joins, s_side[2];                  // joins; those of the units shared with the CTAs before and behind
-  __shared__ int s_last[2], s_first[2];               // of these: states if this CTA joins them, first CTA
+  __shared__ int s_last[2];                           // of these: whether this CTA joins the CTAs' states
   __shared__ int s_seqs[kWarps];
   __shared__ OpenState s_open[2 * kWarps];   // of a warp: of the unit it ends, of the unit it leaves unfinished
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -386,10 +402,13 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
   const int c = blockIdx.x;
   // Warp i of them takes [first_of(i), first_of(i + 1)), a tile at least (the host bounds total * n_warps).
   const uint32_t n_warps = static_cast<uint32_t>(max(int64_t{1}, min(static_cast<int64_t>(G) * kWarps, total)));
-  const auto first_of = [&](int i) {
-    return static_cast<int64_t>(static_cast<uint64_t>(total) * min(static_cast<uint32_t>(i), n_warps) / n_warps);
+  const int64_t quot = total >> 32 ? total / n_warps : static_cast<int64_t>(static_cast<uint32_t>(total) / n_warps);
+  const uint32_t rem = static_cast<uint32_t>(total - quot * n_warps);
+  const auto first_of = [&](uint32_t i) {
+    i = min(i, n_warps);
+    return quot * i + rem * i / n_warps;
   };
-  const auto cta_of = [&](int64_t x) {   // the CTA whose range holds x
+  const auto cta_of = [&](int64_t x) {   // of the warp whose range holds x: the last with total * i / n_warps <= x
     return static_cast<int>((static_cast<uint64_t>(x + 1) * n_warps - 1) / static_cast<uint64_t>(total)) / kWarps;
   };
   const int64_t f0 = first_of(c * kWarps), f1 = first_of((c + 1) * kWarps);
@@ -854,58 +873,33 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
     // states behind it.)
     __syncthreads();
     if (lane == 0 && warp < 2) {
-      int n = 0, c0 = 0;
-      if (s_side[warp] >= 0) {
-        const Join& j = s_join[s_side[warp]];
-        c0 = cta_of(j.x0);
+      const int k = s_side[warp];
+      int n = 0;
+      if (k >= 0) {
+        Join& j = s_join[k];
+        const int c0 = cta_of(j.x0);
         n = cta_of(j.x1 - 1) - c0 + 1;
         uint32_t* const count = a.counters + c0;
         uint32_t old;
         asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(count) : "memory");
-        if (old == static_cast<uint32_t>(n - 1))
+        if (old == static_cast<uint32_t>(n - 1)) {
           *count = 0;
-        else
+          // the states of the CTAs behind the first, and the first one's
+          j.base = a.parts + static_cast<size_t>(2 * (c0 + 1)) * a.state;
+          j.last = a.parts + static_cast<size_t>(2 * c0 + 1) * a.state;
+          j.to = nullptr;
+          j.stride = 2 * a.state;
+          j.n = n;
+        } else {
           n = 0;
+        }
       }
       s_last[warp] = n;
-      s_first[warp] = c0;
     }
     __syncthreads();
 #pragma unroll 1
-    for (int side = 0; side < 2; ++side) {
-      const int n = s_last[side], c0 = s_first[side];
-      if (n == 0) continue;
-      Join& j = s_join[s_side[side]];
-      const int words = j.heads * (D + 4);                  // floats of a state
-      // as many at a time as the rings hold behind two slots, which in turn have what was joined before
-      int kept = -1;
-#pragma unroll 1
-      for (int done = 0; done < n;) {
-        const int now = min(n - done, S::kSlots - 2);
-#pragma unroll 1
-        for (int i = warp; i < now; i += kWarps) {
-          const float* const from = a.parts + static_cast<size_t>(2 * (c0 + done + i) + (done + i == 0)) * a.state;
-          const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(rings + (2 + i) * words));
-          for (int k = lane * 4; k < words; k += 128)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k * 4), "l"(from + k) : "memory");
-        }
-        copy_commit();
-        copy_wait<0>();
-        done += now;
-        __syncthreads();
-        if (tid == 0) {
-          j.base = rings + 2 * words;
-          j.last = kept < 0 ? nullptr : rings + kept * words;
-          j.to = done < n ? rings + (kept != 0 ? 0 : words) : nullptr;
-          j.stride = words;
-          j.n = now + (kept >= 0);
-        }
-        kept = kept != 0 ? 0 : 1;
-        __syncthreads();
-        join_states<TQ, D, kThreads>(a, &j, 1);
-        __syncthreads();
-      }
-    }
+    for (int side = 0; side < 2; ++side)
+      if (s_last[side]) join_states<TQ, D, kThreads>(a, s_join + s_side[side], 1);
   }
 
   // Rows of sequences without tokens, and lengths out of range.
