@@ -37,8 +37,8 @@ int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64
   if (B < 0 || window < 0 || !std::isfinite(scale)) return HHR_ERR_INVALID_ARG;
   if (out_type != c.q_type && out_type != HHR_TYPE_F32) return HHR_ERR_INVALID_ARG;
   if (static_cast<int64_t>(B) * c.Hq >= (int64_t{1} << 31)) return HHR_ERR_UNSUPPORTED;
-  // tiles of the call x warps of the card stay below 2^63
-  if (static_cast<double>(B) * c.Hq * (static_cast<double>(c.table_cols) * c.page / 16 + 1) >= 0x1p51) return HHR_ERR_UNSUPPORTED;
+  // a warp's tiles are counted in 32 bits
+  if (static_cast<double>(B) * c.Hq * (static_cast<double>(c.table_cols) * c.page / 16 + 1) >= 0x1p36) return HHR_ERR_UNSUPPORTED;
   if (!workspace || !aligned_to(workspace, 256) || ws_bytes < hhr_paged_workspace_size(cache)) return HHR_ERR_WORKSPACE;
   if (B == 0) return HHR_OK;
   if (!q || !K || !V || !table || !lens || !out) return HHR_ERR_INVALID_ARG;
@@ -67,7 +67,8 @@ int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64
   a.v_page = c.v_page * size;
   a.v_head = c.v_head * size;
   a.v_tok = c.v_tok * size;
-  a.scale_log2 = scale * c.k_scale * 1.4426950408889634f;
+  a.scale_log2 = std::fabs(scale) * c.k_scale * 1.4426950408889634f;
+  a.flip = scale < 0 ? 0x80008000u : 0;
   a.v_scale = c.v_scale;
   a.B = B;
   a.Hq = c.Hq;

@@ -22,11 +22,12 @@
 // entry serves all of them.
 //
 // Products.  S^T = K Q^T (m16n8k16, tokens by heads: 8 heads fill n where a tile of 16 query rows would be half empty)
-// and O^T += V^T P^T, float32 sums; P is the exact-to-2^-16 sum of two 16-bit values (2^-9 of P alone would show in a
-// float32 output).  8-bit elements become fp16 in registers, exactly; bf16 queries of an 8-bit cache become fp16 after
-// a power of two per row that makes their largest element about 2^14 (elements below 2^-28 of it lose bits).  mma.sync
-// and not tcgen05: a tile is 16 tokens of one warp, whose P never leaves its registers; the tensor pipe has room to
-// spare, and a 128-row tile with its commits would couple the warps that the private rings keep apart.
+// and O^T += V^T P^T, float32 sums.  P is a sum of two 16-bit values, exact to 2^-16 (bf16's 2^-8 alone would show in the
+// output); with an 8-bit cache and a bf16 output it is one fp16 value (2^-11, an eighth of the output's own rounding).
+// 8-bit elements become fp16 in registers, exactly; bf16 queries of an 8-bit cache become fp16 after a power of two per
+// row that makes their largest element about 2^14 (elements below 2^-28 of it lose bits).  mma.sync and not tcgen05: a
+// tile is 16 tokens of one warp, whose P never leaves its registers; the tensor pipe has room to spare, and a 128-row
+// tile with its commits would couple the warps that the private rings keep apart.
 #pragma once
 
 #include <algorithm>
@@ -54,7 +55,8 @@ struct PagedArgs {
   float* firsts;               // [kPagedMaxGrid][kPagedMaxWarps]: states of the units that a warp ends and did not begin
   int64_t q_seq;                                              // elements
   int64_t k_page, k_head, k_tok, v_page, v_head, v_tok;       // bytes
-  float scale_log2, v_scale;
+  float scale_log2, v_scale;   // |scale| k_scale log2(e)
+  uint32_t flip;               // the signs of two 16-bit values if the scale is negative: the queries take it
   int B, Hq, Hkv, page, n_pages, table_cols, table_stride, window, out_f32;
   int r, chunk, chunks;        // query heads of a KV head, of a unit (at most 8 NT), and units of a KV head
   int state;                   // floats of a state
@@ -318,7 +320,7 @@ __device__ __noinline__ void join_states(const PagedArgs& a, const Join* joins, 
   }
 }
 
-template <typename TQ, typename TC, int D, int NT>
+template <typename TQ, typename TC, int D, int NT, bool kPair>
 __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_kernel(const PagedArgs a) {
   using S = PagedShape<TQ, TC, D, NT>;
   using TM = typename S::TM;
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
     const unsigned char* const Kb = static_cast<const unsigned char*>(a.K) + chunk0 * 16 + row0 * a.k_tok;
     const unsigned char* const Vb = static_cast<const unsigned char*>(a.V) + chunk0 * 16 + row0 * a.v_tok;
     TileCursor ld = seg;
-    int64_t ld_left = w1 - w0;   // tiles that have not been asked for
+    int ld_left = static_cast<int>(w1 - w0);   // tiles that have not been asked for
     const unsigned char *Kh = Kb, *Vh = Vb;   // of the tile's KV head
     int id = 0, in_page = 0;     // of the tile's row `lane` (of the first of its 16 rows, if whole)
     uint32_t mask = 0;           // the tile's rows that are tokens
@@ -477,14 +479,13 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
     const uint64_t policy = read_once();
     const uint32_t lane_c = turn<kRow>(row0, chunk0);
     const auto copy_to = [&](uint32_t dst, int j) { return dst + (lane_c ^ ((j * kRows & 7) << 4)) + j * kRows * kRow; };
-    const auto copy_rows = [&](uint32_t dst, const unsigned char* base, int64_t page, int64_t tok) {
+    // rows at base + the lane's offset of each (whole: of each 16)
+    const auto copy_rows = [&](uint32_t dst, const unsigned char* base, int64_t off, int64_t tok) {
       if (whole) {
         const int64_t step = tok * kRows;
 #pragma unroll
         for (int m = 0; m < kSub; ++m) {
-          const int mid = kSub == 1 ? id : __shfl_sync(~0u, id, 16 * m);
-          const int off = kSub == 1 ? in_page : __shfl_sync(~0u, in_page, 16 * m);
-          const unsigned char* src = base + (mid * page + off * tok);
+          const unsigned char* src = base + (kSub == 1 ? off : __shfl_sync(~0u, off, 16 * m));
           constexpr int kEach = kCopies / kSub;
           if (live == kAll) {
 #pragma unroll
@@ -500,9 +501,9 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
 #pragma unroll
         for (int j = 0; j < kCopies; ++j) {
           const int row = j * kRows + row0;
-          const int64_t rid = __shfl_sync(~0u, id, row), rin = __shfl_sync(~0u, in_page, row);
+          const int64_t at = __shfl_sync(~0u, off, row);
           const bool on = (live >> row) & 1;
-          copy16(copy_to(dst, j), on ? first + (rid * page + rin * tok) : first, policy, on);
+          copy16(copy_to(dst, j), on ? first + at : first, policy, on);
         }
       }
     };
@@ -511,18 +512,18 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
       if (ld_left > 0) {
         const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.n_pages);
         live = mask & __ballot_sync(~0u, ok);
-        if (!ok) id = 0;
+        if (!ok) id = in_page = 0;
         if (lane == 0) {
           masks[slot] = live;
           if (live != mask) *a.status = HHR_ERR_BAD_INDEX;
         }
-        copy_rows(ring + slot * 2 * kTile, Kh, a.k_page, a.k_tok);
+        copy_rows(ring + slot * 2 * kTile, Kh, id * a.k_page + in_page * a.k_tok, a.k_tok);
       }
       copy_commit();
     };
     const auto issue_v = [&](int slot) {
       if (ld_left > 0) {
-        copy_rows(ring + slot * 2 * kTile + kTile, Vh, a.v_page, a.v_tok);
+        copy_rows(ring + slot * 2 * kTile + kTile, Vh, id * a.v_page + in_page * a.v_tok, a.v_tok);
         if (--ld_left > 0) {
           ld.next<kTokens>(a, units);
           find();
@@ -566,13 +567,13 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
           for (int k = 0; k < D / 16; ++k) {
             if constexpr (S::kE4) {
               const uint2 x = *reinterpret_cast<const uint2*>(row + k * 16 + 4 * t4);
-              qf[k][n][0] = on ? x.x : 0;
-              qf[k][n][1] = on ? x.y : 0;
+              qf[k][n][0] = on ? x.x ^ a.flip : 0;
+              qf[k][n][1] = on ? x.y ^ a.flip : 0;
             } else {
               const uint32_t x = *reinterpret_cast<const uint32_t*>(row + k * 16 + 2 * t4);
               const uint32_t y = *reinterpret_cast<const uint32_t*>(row + k * 16 + 8 + 2 * t4);
-              qf[k][n][0] = on ? x : 0;
-              qf[k][n][1] = on ? y : 0;
+              qf[k][n][0] = on ? x ^ a.flip : 0;
+              qf[k][n][1] = on ? y ^ a.flip : 0;
             }
           }
         } else {   // bf16 queries of an 8-bit cache
@@ -580,8 +581,8 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint2 x = *reinterpret_cast<const uint2*>(row + k * 16 + 4 * t4);
-            qf[k][n][0] = on ? x.x : 0;
-            qf[k][n][1] = on ? x.y : 0;
+            qf[k][n][0] = on ? x.x ^ a.flip : 0;
+            qf[k][n][1] = on ? x.y ^ a.flip : 0;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qf[k][n][e]));
@@ -605,8 +606,8 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           sc[n][e] = __shfl_sync(~0u, up, (2 * t4 + e) * 4);
-          m[n][e] = -INFINITY;
-          base[n][e] = l[n][e] = 0;
+          m[n][e] = -INFINITY;        // the largest product so far
+          base[n][e] = l[n][e] = 0;   // weights are 2^(product * sc - base) with base = m * sc - kLift
         }
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
@@ -672,15 +673,18 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
         __syncwarp();
         issue_k(slot);
         // weights: lane (g, t4) holds tokens g and g + 8 of heads 2 t4 and 2 t4 + 1
+        const bool some = rows != kAll;
         bool grown = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < kSub; ++i) {
             float(&x)[4] = s[i][0][n];
+            if constexpr (kSums == 2) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = (kSums == 2 ? x[e] + s[i][kSums - 1][n][e] : x[e]) * sc[n][e & 1];
-            if (rows != kAll) {
+              for (int e = 0; e < 4; ++e) x[e] += s[i][kSums - 1][n][e];
+            }
+            if (some) {
               if (!((rows >> (16 * i + g)) & 1)) x[0] = x[1] = -INFINITY;
               if (!((rows >> (16 * i + g + 8)) & 1)) x[2] = x[3] = -INFINITY;
             }
@@ -698,14 +702,18 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
               top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
               top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
               top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
-              const float by = top == m[n][e] ? 1.0f : ex2(m[n][e] - top);
-              m[n][e] = top;
-              base[n][e] = top == -INFINITY ? 0.0f : top - kLift;
-              l[n][e] *= by;
+              if (top > m[n][e]) {   // the same for the 8 lanes of a column
+                // rounded as the logits below are: at the size of a mask by the lowest value the rounding is no small thing
+                const float next = __fmul_rn(top, sc[n][e]) - kLift;
+                const float by = m[n][e] == -INFINITY ? 1.0f : ex2(base[n][e] - next);
+                m[n][e] = top;
+                base[n][e] = next;
+                l[n][e] *= by;
 #pragma unroll
-              for (int j = 0; j < D / 16; ++j) {
-                o[n][j][e] *= by;
-                o[n][j][e + 2] *= by;
+                for (int j = 0; j < D / 16; ++j) {
+                  o[n][j][e] *= by;
+                  o[n][j][e + 2] *= by;
+                }
               }
             }
         }
@@ -716,14 +724,18 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
           for (int i = 0; i < kSub; ++i) {
             float w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = ex2(s[i][0][n][e] - base[n][e & 1]);
+            for (int e = 0; e < 4; ++e) w[e] = ex2(__fmul_rn(s[i][0][n][e], sc[n][e & 1]) - base[n][e & 1]);
+            if (some) {   // (a scale of zero makes them numbers)
+              if (!((rows >> (16 * i + g)) & 1)) w[0] = w[1] = 0;
+              if (!((rows >> (16 * i + g + 8)) & 1)) w[2] = w[3] = 0;
+            }
             l[n][0] += w[0] + w[2];
             l[n][1] += w[1] + w[3];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               split<TM>(w[2 * e], w[2 * e + 1], hi[i][n][e], lo[i][n][e]);
               hi[i][n][e] = transposed(hi[i][n][e]);
-              lo[i][n][e] = transposed(lo[i][n][e]);
+              if constexpr (kPair) lo[i][n][e] = transposed(lo[i][n][e]);
             }
           }
         copy_wait<kLead>();
@@ -737,7 +749,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
                 mma<TM>(o[n][to], r, hi[i][n][0], hi[i][n][1]);
-                mma<TM>(o[n][to], r, lo[i][n][0], lo[i][n][1]);
+                if constexpr (kPair) mma<TM>(o[n][to], r, lo[i][n][0], lo[i][n][1]);
               }
             };
             uint32_t r[4];
@@ -924,11 +936,11 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
 }
 
 // Launches the variant for D and the heads of a unit.
-template <typename TQ, typename TC, int D, int NT>
+template <typename TQ, typename TC, int D, int NT, bool kPair>
 cudaError_t launch_paged_kernel(const PagedArgs& a, int grid, cudaStream_t s) {
   using S = PagedShape<TQ, TC, D, NT>;
   static std::atomic<size_t> raised[kMaxDevices];
-  const auto kern = paged_kernel<TQ, TC, D, NT>;
+  const auto kern = paged_kernel<TQ, TC, D, NT, kPair>;
   if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), S::kSmem, raised)) return e;
   return launch_dependent<PagedArgs>(kern, dim3(grid), S::kThreads, S::kSmem, s, a);
 }
@@ -936,22 +948,29 @@ cudaError_t launch_paged_kernel(const PagedArgs& a, int grid, cudaStream_t s) {
 // Most heads of a unit, by the registers of its sums: D / 16 x 4 floats a lane for 8 heads.
 inline int paged_max_heads(int d) { return d == 64 ? 32 : d == 128 ? 24 : 16; }
 
+template <typename TQ, typename TC, int D, int NT>
+cudaError_t launch_paged_pair(const PagedArgs& a, int grid, cudaStream_t s) {
+  if constexpr (std::is_same<TQ, __nv_bfloat16>::value && sizeof(TC) == 1)
+    if (!a.out_f32) return launch_paged_kernel<TQ, TC, D, NT, false>(a, grid, s);
+  return launch_paged_kernel<TQ, TC, D, NT, true>(a, grid, s);
+}
+
 template <typename TQ, typename TC>
 cudaError_t launch_paged_typed(const PagedArgs& a, int d, int grid, cudaStream_t s) {
   const int nt = (a.chunk + 7) / 8;
   if (d == 64) {
-    if (nt == 1) return launch_paged_kernel<TQ, TC, 64, 1>(a, grid, s);
-    if (nt == 2) return launch_paged_kernel<TQ, TC, 64, 2>(a, grid, s);
-    if (nt == 3) return launch_paged_kernel<TQ, TC, 64, 3>(a, grid, s);
-    return launch_paged_kernel<TQ, TC, 64, 4>(a, grid, s);
+    if (nt == 1) return launch_paged_pair<TQ, TC, 64, 1>(a, grid, s);
+    if (nt == 2) return launch_paged_pair<TQ, TC, 64, 2>(a, grid, s);
+    if (nt == 3) return launch_paged_pair<TQ, TC, 64, 3>(a, grid, s);
+    return launch_paged_pair<TQ, TC, 64, 4>(a, grid, s);
   }
   if (d == 128) {
-    if (nt == 1) return launch_paged_kernel<TQ, TC, 128, 1>(a, grid, s);
-    if (nt == 2) return launch_paged_kernel<TQ, TC, 128, 2>(a, grid, s);
-    return launch_paged_kernel<TQ, TC, 128, 3>(a, grid, s);
+    if (nt == 1) return launch_paged_pair<TQ, TC, 128, 1>(a, grid, s);
+    if (nt == 2) return launch_paged_pair<TQ, TC, 128, 2>(a, grid, s);
+    return launch_paged_pair<TQ, TC, 128, 3>(a, grid, s);
   }
-  if (nt == 1) return launch_paged_kernel<TQ, TC, 256, 1>(a, grid, s);
-  return launch_paged_kernel<TQ, TC, 256, 2>(a, grid, s);
+  if (nt == 1) return launch_paged_pair<TQ, TC, 256, 1>(a, grid, s);
+  return launch_paged_pair<TQ, TC, 256, 2>(a, grid, s);
 }
 
 // One translation unit per pair of types (paged_*.cu).

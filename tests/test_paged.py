@@ -5,7 +5,7 @@ Tolerances.  An appended element is the rotated one's float32 value (12 half ste
 test_rope.py) rounded once to the cache's type.  For attention let w_n be the softmax weights: the logits' float32
 error is at most (d + 4) 2^-24 scale sum_e |q_e k_e| =: e_n for a d-term sum in any order and its scaling, which moves
 each weight by a factor exp(+-2 max_n e_n); weights, sums and merges round to float32 (or a pair of 16-bit values that
-holds 2^-16), so with c = 2^-15 + 2 max e_n the output is within (c + 2^-24 rounds) sum_n w_n |v_n| + its own rounding.
+holds 2^-16; with a bf16 output of an 8-bit cache one fp16 value, 2^-11), so with c = 2^-15 (or 2^-11 + 2^-15) + 2 max e_n the output is within (c + 2^-24 rounds) sum_n w_n |v_n| + its own rounding.
 The growth of float32 sums over n tokens is covered by 2^-24 (tokens of one lane + merges) <= 2^-24 (n / 16 + 64).  The
 log-sum-exp is within max e_n + 2^-24 (n / 16 + 64) + 2^-22 |lse|."""
 import ctypes as C
@@ -149,6 +149,7 @@ def attend64(cache, q, table, lens, window=0, scale=None, scales=(1.0, 1.0), liv
     scale = 1.0 / math.sqrt(d) if scale is None else scale
     q = q.double().cpu()
     out, tol = torch.zeros(B, Hq, d, dtype=torch.float64), torch.zeros(B, Hq, d, dtype=torch.float64)
+    mag = torch.zeros(B, Hq, d, dtype=torch.float64)
     lse, ltol = torch.full((B, Hq), -math.inf, dtype=torch.float64), torch.zeros(B, Hq, dtype=torch.float64)
     for b, n in enumerate(lens.tolist()):
         lo = max(0, n - window) if window else 0
@@ -166,13 +167,16 @@ def attend64(cache, q, table, lens, window=0, scale=None, scales=(1.0, 1.0), liv
             w = torch.exp(x - lse[b, h])
             out[b, h] = w @ v[:, h // r]
             sums = 2.0 ** -24 * (k.shape[0] / 16 + 64)
-            tol[b, h] = (2.0 ** -15 + 2 * e + sums) * (w @ v[:, h // r].abs())
+            mag[b, h] = w @ v[:, h // r].abs()
+            tol[b, h] = (2.0 ** -15 + 2 * e + sums) * mag[b, h]
             ltol[b, h] = e + sums + 2.0 ** -22 * lse[b, h].abs()
-    return out, lse, tol, ltol
+    return out, lse, tol, ltol, mag
 
 
-def compare(out, lse, want, name=""):
-    o, l, tol, ltol = want
+def compare(out, lse, want, name="", rounded=0.0):
+    """rounded: what the weights' own rounding adds, relative to sum w |v| (attend64 has 2^-15 of it)."""
+    o, l, tol, ltol, mag = want
+    tol = tol + rounded * mag
     half = HALF[out.dtype]
     err = (out.double().cpu() - o).abs()
     limit = half * o.abs() + tol * (1 + half) + (2.0 ** -25 if out.dtype == FP16 else 0.0)
@@ -200,7 +204,8 @@ def make(B, Hq, Hkv, d, page, cols, *, dtype=BF, kv=None, layout="head", seed=0,
     return c, q.to(dtype).cuda(), table
 
 
-def run(c, q, table, lens, *, window=0, out_dtype=None, scales=(1.0, 1.0), name="", **kw):
+def run(c, q, table, lens, *, window=0, out_dtype=None, scales=(1.0, 1.0), name="", low=None, **kw):
+    """low: tokens whose weight is zero by their logits' size (left out of the tolerance's largest logit)."""
     lens = torch.as_tensor(lens, dtype=torch.int32, device="cuda")
     out = torch.full(q.shape, float("nan"), dtype=out_dtype or q.dtype, device="cuda")
     lse = torch.full(q.shape[:2], float("nan"), dtype=F32, device="cuda")
@@ -208,7 +213,8 @@ def run(c, q, table, lens, *, window=0, out_dtype=None, scales=(1.0, 1.0), name=
     assert got is out
     torch.cuda.synchronize()
     assert c.status() == hhr.HHR_OK
-    compare(out, lse, attend64(c, q, table, lens, window, kw.get("scale"), scales), name)
+    compare(out, lse, attend64(c, q, table, lens, window, kw.get("scale"), scales, None if low is None else [~low]), name,
+            2.0 ** -11 if c.K.dtype == E4 and out.dtype == BF else 0.0)
     return out, lse
 
 
@@ -346,6 +352,30 @@ def test_attend_extreme_values():
     c.K[int(t[0, 2]), 0, 1, 0] = math.nan
     c.attend(q2, t, torch.tensor([100], dtype=torch.int32, device="cuda"), out=out, lse=lse)
     assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_lowest_values_beside_ordinary_ones(d):
+    """Keys that give the type's lowest logits in whole tiles before, between and behind ordinary ones: the ordinary
+    ones keep their differences."""
+    c, q, t = make(1, 4, 1, d, 16, 60)
+    q[..., 0] = 1.0
+    at = torch.arange(960)
+    low = (at < 100) | ((at >= 300) & (at < 500)) | (at % 7 == 3) | (at > 900)
+    n = torch.nonzero(low)[:, 0]
+    c.K[t[0].cpu()[n // 16].long().cuda(), 0, (n % 16).cuda(), 0] = torch.finfo(BF).min
+    run(c, q, t, [960], out_dtype=F32, low=low)
+    run(c, q, t, [95], out_dtype=F32, low=None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1e-30, 3.0])
+@pytest.mark.parametrize("kv", [BF, E4])
+def test_attend_scales(scale, kv):
+    scales = (2.0 ** -5, 2.0 ** -5) if kv == E4 else (1.0, 1.0)
+    c, q, t = make(2, 6, 2, 64, 16, 20, kv=kv, scales=scales)
+    run(c, q, t, [301, 7], out_dtype=F32, scale=scale, scales=scales)
 
 
 @pytest.mark.gpu
