@@ -78,10 +78,11 @@ struct PagedShape {
   static constexpr int kTokens = 16 * kSub;
   static constexpr int kTile = kTokens * kRow;
   static constexpr int kHeads = 8 * NT;
-  // registers hold the query fragments unless the sums leave no room: then each warp reads them from shared memory
-  static constexpr bool kQRegs = D / 16 * NT * 2 <= 48;
+  // Registers hold the query fragments of 8 heads; those of more are read from shared memory, each warp its own copy
+  // (16 heads, d = 128, 8-bit: 58 us in registers of 8 warps, 55 of 12 warps with spills, 53 from shared memory).
+  static constexpr bool kQRegs = NT == 1;
   // More warps hide more latency where their registers allow it.
-  static constexpr int kWarps = D * NT <= 128 ? 12 : 8;
+  static constexpr int kWarps = D < 256 && NT <= 2 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kDepth = std::max(1, 131072 / (kWarps * 2 * kTile));
   // shared memory

@@ -73,32 +73,79 @@ __device__ __forceinline__ void store(TO* p, const float (&f)[V], float mul) {
   *reinterpret_cast<Pack<TO, V>*>(p) = r;
 }
 
+// Where the pair (cos, sin) of element e of a place lies among the angles of a block: the 16-byte pieces (two pairs) of
+// a place stand `turns` pieces apart, so that the places of a row read them from different banks.
+template <int V>
+__device__ __forceinline__ int angle_at(int t, int half, int turns, int place, int e) {
+  return V == 1 ? 2 * (t * half + place) : 2 * t * half + ((e >> 1) * turns + place) * 4 + (e & 1) * 2;
+}
+
 // TI: type of x, y, k, v; TC: cache type; V: elements per access; U: rows a
 // thread has in flight.
 template <typename TI, typename TC, int V, int U>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int half = a.rot >> 1;
-  float2* cs = reinterpret_cast<float2*>(smem);                           // [tokens_block][half]
-  int64_t* slot = reinterpret_cast<int64_t*>(cs + static_cast<size_t>(a.tokens_block) * half);  // K offset, V offset
+  float* cs = reinterpret_cast<float*>(smem);                             // [tokens_block][half] (cos, sin), see angle_at
+  int64_t* slot = reinterpret_cast<int64_t*>(cs + static_cast<size_t>(a.tokens_block) * a.rot);  // K offset, V offset
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows_block;
   const int64_t rows_all = static_cast<int64_t>(a.T) * a.heads;
   const int rows = static_cast<int>(min(static_cast<int64_t>(a.rows_block), rows_all - row0));
   const int tok0 = static_cast<int>(static_cast<uint32_t>(row0) / static_cast<uint32_t>(a.heads));
   const int tok_n = static_cast<int>(static_cast<uint32_t>(row0 + rows - 1) / static_cast<uint32_t>(a.heads)) - tok0 + 1;
 
+  const int I = a.places;
+  const int place = threadIdx.x % I, first = threadIdx.x / I;
+  const bool idle = first >= kRopeThreads / I;
+  const bool turned = place * 2 * V < a.rot;
+  // element places of the two halves of this thread's 2V elements
+  const int p0 = turned && !a.interleaved ? place * V : place * 2 * V;
+  const int p1 = turned && !a.interleaved ? half + place * V : place * 2 * V + V;
+  const int turns = half / V;   // places that are turned
+
   dependency_wait();
   launch_dependents();
+
+  // this thread's rows: U heads in a row, mostly of one token, all asked for before the angles are computed
+  Pack<TI, V> x0[U], x1[U];
+  int tok[U], head[U];
+  bool live[U];
+  {
+    uint32_t row = static_cast<uint32_t>(row0) + static_cast<uint32_t>(min(first * U, rows - 1));
+    int t = static_cast<int>(row / static_cast<uint32_t>(a.heads));
+    int h = static_cast<int>(row - static_cast<uint32_t>(t) * static_cast<uint32_t>(a.heads));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      tok[u] = t;
+      head[u] = h;
+      live[u] = !idle && first * U + u < rows && (h >= a.H || turned || a.tail);
+      if (live[u]) {
+        const TI* p;
+        if (h < a.H)
+          p = static_cast<const TI*>(a.x) + t * a.x_tok + h * a.x_head;
+        else if (h < a.H + a.Hkv)
+          p = static_cast<const TI*>(a.k) + t * a.k_row + static_cast<int64_t>(h - a.H) * a.d;
+        else
+          p = static_cast<const TI*>(a.v) + t * a.v_row + static_cast<int64_t>(h - a.H - a.Hkv) * a.d;
+        load<TI, V>(p + p0, x0[u]);
+        load<TI, V>(p + p1, x1[u]);
+      }
+      if (++h == a.heads) {
+        h = 0;
+        ++t;
+      }
+    }
+  }
 
   // the angles of the block's tokens
   for (int i = threadIdx.x; i < tok_n * half; i += kRopeThreads) {
     const int t = i / half, j = i - t * half;
     const int p = (a.rope_pos ? a.rope_pos : a.pos)[tok0 + t];
-    const double turns = static_cast<double>(p) * a.freqs[j] * 0.15915494309189533577;
-    const float r = static_cast<float>(2.0 * (turns - rint(turns)));
+    const double turn = static_cast<double>(p) * a.freqs[j] * 0.15915494309189533577;
+    const float r = static_cast<float>(2.0 * (turn - rint(turn)));
     float s, c;
     sincospif(r, &s, &c);
-    cs[i] = make_float2(a.mscale * c, a.sign * a.mscale * s);
+    *reinterpret_cast<float2*>(cs + angle_at<V>(t, half, turns, j / V, j % V)) = make_float2(a.mscale * c, a.sign * a.mscale * s);
   }
   // the places of the block's tokens in the cache: element offsets of K and V,
   // or -1 for a token that is not written
@@ -123,106 +170,88 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   }
   __syncthreads();
 
-  const int I = a.places;
-  const int step = kRopeThreads / I;
-  const int place = threadIdx.x % I, first = threadIdx.x / I;
-  if (first >= step) return;
-  const bool turned = place * 2 * V < a.rot;
-  // element places of the two halves of this thread's 2V elements
-  const int p0 = turned && !a.interleaved ? place * V : place * 2 * V;
-  const int p1 = turned && !a.interleaved ? half + place * V : place * 2 * V + V;
-
-  for (int r0 = first; r0 < rows; r0 += step * U) {
-    Pack<TI, V> x0[U], x1[U];
-    int tok[U], head[U];
-    bool live[U];
+  float w[2 * V];       // cosines and sines of this place, of token `have`
+  int have = -1;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * step;
-      const uint32_t row = static_cast<uint32_t>(row0) + static_cast<uint32_t>(min(r, rows - 1));
-      tok[u] = static_cast<int>(row / static_cast<uint32_t>(a.heads));
-      head[u] = static_cast<int>(row - static_cast<uint32_t>(tok[u]) * static_cast<uint32_t>(a.heads));
-      live[u] = r < rows && (a.Hkv == 0 || slot[2 * (tok[u] - tok0)] >= 0);
-      if (head[u] < a.H) live[u] = live[u] && (turned || a.tail);
-      if (live[u]) {
-        const TI* p;
-        if (head[u] < a.H)
-          p = static_cast<const TI*>(a.x) + tok[u] * a.x_tok + head[u] * a.x_head;
-        else if (head[u] < a.H + a.Hkv)
-          p = static_cast<const TI*>(a.k) + tok[u] * a.k_row + static_cast<int64_t>(head[u] - a.H) * a.d;
-        else
-          p = static_cast<const TI*>(a.v) + tok[u] * a.v_row + static_cast<int64_t>(head[u] - a.H - a.Hkv) * a.d;
-        load<TI, V>(p + p0, x0[u]);
-        load<TI, V>(p + p1, x1[u]);
+  for (int u = 0; u < U; ++u) {
+    const int t = tok[u] - tok0;
+    if (!live[u] || (a.Hkv && slot[2 * t] < 0)) continue;
+    const bool is_q = head[u] < a.H, is_v = head[u] >= a.H + a.Hkv;
+    TI* yq = static_cast<TI*>(a.y) + tok[u] * a.y_tok + head[u] * a.y_head;
+    TC* yc = is_v ? static_cast<TC*>(a.V) + slot[2 * t + 1] + (head[u] - a.H - a.Hkv) * a.v_head
+                  : static_cast<TC*>(a.K) + slot[2 * t] + (head[u] - a.H) * a.k_head;
+    if (is_v || !turned) {
+      if (is_q) {
+        *reinterpret_cast<Pack<TI, V>*>(yq + p0) = x0[u];
+        *reinterpret_cast<Pack<TI, V>*>(yq + p1) = x1[u];
+      } else if constexpr (sizeof(TC) == sizeof(TI)) {   // the same type: the bits as they are
+        *reinterpret_cast<Pack<TI, V>*>(yc + p0) = x0[u];
+        *reinterpret_cast<Pack<TI, V>*>(yc + p1) = x1[u];
+      }
+      if constexpr (sizeof(TC) != sizeof(TI)) {
+        if (!is_q) {
+          float f0[V], f1[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            f0[e] = to_f32(x0[u].v[e]);
+            f1[e] = to_f32(x1[u].v[e]);
+          }
+          store<TC, V>(yc + p0, f0, is_v ? a.v_inv : a.k_inv);
+          store<TC, V>(yc + p1, f1, is_v ? a.v_inv : a.k_inv);
+        }
+      }
+      continue;
+    }
+    if (have != t) {
+      have = t;
+      if constexpr (V == 1) {
+        const float2 z = *reinterpret_cast<const float2*>(cs + angle_at<V>(t, half, turns, place, 0));
+        w[0] = z.x;
+        w[1] = z.y;
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          const float4 z = *reinterpret_cast<const float4*>(cs + angle_at<V>(t, half, turns, place, e));
+          w[2 * e] = z.x;
+          w[2 * e + 1] = z.y;
+          w[2 * e + 2] = z.z;
+          w[2 * e + 3] = z.w;
+        }
       }
     }
+    float f0[V], f1[V];
+    if (a.interleaved) {
+      float g[2 * V];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (!live[u]) continue;
-      const int t = tok[u] - tok0;
-      const bool is_q = head[u] < a.H, is_v = head[u] >= a.H + a.Hkv;
-      TI* yq = static_cast<TI*>(a.y) + tok[u] * a.y_tok + head[u] * a.y_head;
-      TC* yc = is_v ? static_cast<TC*>(a.V) + slot[2 * t + 1] + (head[u] - a.H - a.Hkv) * a.v_head
-                    : static_cast<TC*>(a.K) + slot[2 * t] + (head[u] - a.H) * a.k_head;
-      if (is_v || !turned) {
-        if (is_q) {
-          *reinterpret_cast<Pack<TI, V>*>(yq + p0) = x0[u];
-          *reinterpret_cast<Pack<TI, V>*>(yq + p1) = x1[u];
-        } else if constexpr (sizeof(TC) == sizeof(TI)) {   // the same type: the bits as they are
-          *reinterpret_cast<Pack<TI, V>*>(yc + p0) = x0[u];
-          *reinterpret_cast<Pack<TI, V>*>(yc + p1) = x1[u];
-        }
-        if constexpr (sizeof(TC) != sizeof(TI)) {
-          if (!is_q) {
-            float f0[V], f1[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              f0[e] = to_f32(x0[u].v[e]);
-              f1[e] = to_f32(x1[u].v[e]);
-            }
-            store<TC, V>(yc + p0, f0, is_v ? a.v_inv : a.k_inv);
-            store<TC, V>(yc + p1, f1, is_v ? a.v_inv : a.k_inv);
-          }
-        }
-        continue;
+      for (int e = 0; e < V; ++e) {
+        g[e] = to_f32(x0[u].v[e]);
+        g[V + e] = to_f32(x1[u].v[e]);
       }
-      const float2* c = cs + t * half + place * V;
-      float f0[V], f1[V];
-      if (a.interleaved) {
-        float g[2 * V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          g[e] = to_f32(x0[u].v[e]);
-          g[V + e] = to_f32(x1[u].v[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float2 w = c[e];
-          const float u1 = g[2 * e], u2 = g[2 * e + 1];
-          g[2 * e] = fmaf(u1, w.x, -(u2 * w.y));
-          g[2 * e + 1] = fmaf(u2, w.x, u1 * w.y);
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          f0[e] = g[e];
-          f1[e] = g[V + e];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float2 w = c[e];
-          const float u1 = to_f32(x0[u].v[e]), u2 = to_f32(x1[u].v[e]);
-          f0[e] = fmaf(u1, w.x, -(u2 * w.y));
-          f1[e] = fmaf(u2, w.x, u1 * w.y);
-        }
+      for (int e = 0; e < V; ++e) {
+        const float u1 = g[2 * e], u2 = g[2 * e + 1];
+        g[2 * e] = fmaf(u1, w[2 * e], -(u2 * w[2 * e + 1]));
+        g[2 * e + 1] = fmaf(u2, w[2 * e], u1 * w[2 * e + 1]);
       }
-      if (is_q) {
-        store<TI, V>(yq + p0, f0, 1.0f);
-        store<TI, V>(yq + p1, f1, 1.0f);
-      } else {
-        store<TC, V>(yc + p0, f0, a.k_inv);
-        store<TC, V>(yc + p1, f1, a.k_inv);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        f0[e] = g[e];
+        f1[e] = g[V + e];
       }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float u1 = to_f32(x0[u].v[e]), u2 = to_f32(x1[u].v[e]);
+        f0[e] = fmaf(u1, w[2 * e], -(u2 * w[2 * e + 1]));
+        f1[e] = fmaf(u2, w[2 * e], u1 * w[2 * e + 1]);
+      }
+    }
+    if (is_q) {
+      store<TI, V>(yq + p0, f0, 1.0f);
+      store<TI, V>(yq + p1, f1, 1.0f);
+    } else {
+      store<TC, V>(yc + p0, f0, a.k_inv);
+      store<TC, V>(yc + p1, f1, a.k_inv);
     }
   }
 }

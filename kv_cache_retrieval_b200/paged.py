@@ -8,12 +8,13 @@ sequence comes with each call.
 """
 from __future__ import annotations
 
+import ctypes as C
 import math
 
 import torch
 
 from . import _binding as B
-from .rope import check_tensor, on_device
+from .rope import check_vector, on_device, rotation
 
 _TYPES = {torch.bfloat16: B.HHR_TYPE_BF16, torch.float16: B.HHR_TYPE_F16, torch.float32: B.HHR_TYPE_F32,
           torch.float8_e4m3fn: B.HHR_TYPE_E4M3}
@@ -44,8 +45,10 @@ class HHRPagedCache:
             pages = K.shape[0] if pages is None else pages
             kv_dtype = K.dtype if kv_dtype is None else kv_dtype
             shape = (pages, kv_heads, page, head_dim) if layout == "head" else (pages, page, kv_heads, head_dim)
-            check_tensor("K", K, kv_dtype, K.device, shape)
-            check_tensor("V", V, kv_dtype, K.device, shape)
+            for name, t in (("K", K), ("V", V)):
+                if t.dtype != kv_dtype or t.device != K.device or t.shape != shape:
+                    raise ValueError(f"{name}: expected {kv_dtype} {shape} on {K.device}, "
+                                     f"got {t.dtype} {tuple(t.shape)} on {t.device}")
             if K.stride(3) != 1 or V.stride(3) != 1:
                 raise ValueError("K, V: the elements of a head have to be adjacent")
         if K.dtype not in (dtype, torch.float8_e4m3fn):
@@ -56,6 +59,7 @@ class HHRPagedCache:
         self.desc = B.hhr_paged(q_heads, kv_heads, head_dim, page, pages, 1, 1, _TYPES[dtype], _TYPES[K.dtype],
                                 k_scale, v_scale, 0, *(s.stride(i) for s in (K, V) for i in (0, h, t)))
         self._descs = {}
+        self._index, self._Hq, self._Hkv, self._d = K.get_device(), q_heads, kv_heads, head_dim
         self.workspace = self.new_workspace()
 
     def new_workspace(self):
@@ -67,8 +71,8 @@ class HHRPagedCache:
         return torch.zeros(ws, dtype=torch.uint8, device=self.device)
 
     def _table(self, table):
-        """The description with this table's columns and row stride, and the table's rows."""
-        if table.dim() != 2 or table.dtype != torch.int32 or table.device != self.device or \
+        """A reference to the description with this table's columns and row stride, and the table's rows."""
+        if table.dim() != 2 or table.dtype is not torch.int32 or table.get_device() != self._index or \
                 (table.shape[1] > 1 and table.stride(1) != 1):
             raise ValueError(f"table: expected int32 [sequences, pages] on {self.device} with adjacent columns, "
                              f"got {table.dtype} {tuple(table.shape)} on {table.device}")
@@ -80,18 +84,19 @@ class HHRPagedCache:
             desc.table_cols, desc.table_stride = cols, stride
             if len(self._descs) >= 64:
                 self._descs.clear()
-            self._descs[cols, stride] = desc
+            desc = self._descs[cols, stride] = C.byref(desc)
         return desc, rows
 
     def _rows(self, name, t, heads):
         """Elements between two tokens' rows of t [T, heads, head_dim]."""
-        d = self.desc.d
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype != self.dtype or t.device != self.device:
+        d = self._d
+        if t.dim() != 3 or t.dtype is not self.dtype or t.get_device() != self._index or t.shape[1] != heads or t.shape[2] != d:
             raise ValueError(f"{name}: expected {self.dtype} [tokens, {heads}, {d}] on {self.device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-        if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        row, head, one = t.stride()
+        if one != 1 or (heads > 1 and head != d):
             raise ValueError(f"{name}: a token's heads have to be adjacent")
-        return t.stride(0)
+        return row
 
     def append(self, k, v, positions, table, *, seq=None, q=None, q_out=None, freqs=None, rope_positions=None,
                interleaved=False, mscale=1.0):
@@ -101,33 +106,37 @@ class HHRPagedCache:
         are rotated by rope_positions (None: positions) on the way, and with q
         [T, q_heads, head_dim] the queries too, into q_out (a new tensor if
         None; q itself rotates in place).  Returns q_out."""
-        d, rows = self._table(table)
+        index = self._index
+        desc, rows = self._table(table)
         T = k.shape[0]
-        k_row, v_row = self._rows("k", k, d.Hkv), self._rows("v", v, d.Hkv)
+        k_row, v_row = self._rows("k", k, self._Hkv), self._rows("v", v, self._Hkv)
         if v.shape[0] != T:
             raise ValueError(f"v: {v.shape[0]} tokens, k has {T}")
-        for name, t in (("positions", positions), ("seq", seq), ("rope_positions", rope_positions)):
-            if t is None:
-                continue
-            check_tensor(name, t, torch.int32, self.device, (T,))
-            if T > 1 and t.stride(0) != 1:
-                raise ValueError(f"{name} has to be contiguous")
+        check_vector("positions", positions, torch.int32, T, index)
+        if seq is not None:
+            check_vector("seq", seq, torch.int32, T, index)
+        if rope_positions is not None:
+            check_vector("rope_positions", rope_positions, torch.int32, T, index)
         q_tok = o_tok = 0
         if q is not None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-            q_tok, o_tok = self._rows("q", q, d.Hq), self._rows("q_out", q_out, d.Hq)
+            if q_out is None:
+                q_out = q.new_empty(q.shape)
+            q_tok, o_tok = self._rows("q", q, self._Hq), self._rows("q_out", q_out, self._Hq)
             if q.shape[0] != T or q_out.shape[0] != T:
                 raise ValueError(f"q, q_out: {q.shape[0]} and {q_out.shape[0]} tokens, k has {T}")
         elif q_out is not None:
             raise ValueError("q_out without q")
         rot = None
         if freqs is not None:
-            check_tensor("freqs", freqs, torch.float64, self.device, (freqs.numel(),))
-            if not freqs.is_contiguous():
-                raise ValueError("freqs has to be contiguous")
-            rot = B.hhr_rotation(2 * freqs.numel(), B.HHR_ROPE_INTERLEAVED if interleaved else 0, mscale)
-        on_device(self.device, B.hhr_paged_append, d, T, rows, rot, freqs, positions, rope_positions, seq, table,
-                  q, q_tok, q_out, o_tok, k, k_row, v, v_row, self.K, self.V, self.workspace)
+            check_vector("freqs", freqs, torch.float64, freqs.numel(), index)
+            rot = rotation(2 * freqs.shape[0], B.HHR_ROPE_INTERLEAVED if interleaved else 0, mscale)
+        st = on_device(index, B.lib().hhr_paged_append, desc, T, rows, rot, None if freqs is None else freqs.data_ptr(),
+                       positions.data_ptr(), None if rope_positions is None else rope_positions.data_ptr(),
+                       None if seq is None else seq.data_ptr(), table.data_ptr(), None if q is None else q.data_ptr(), q_tok,
+                       None if q is None else q_out.data_ptr(), o_tok, k.data_ptr(), k_row, v.data_ptr(), v_row,
+                       self.K.data_ptr(), self.V.data_ptr(), self.workspace.data_ptr())
+        if st:
+            raise B.HhrError(st, "hhr_paged_append")
         return q_out
 
     def attend(self, q, table, lens, *, out=None, lse=None, window=0, scale=None, workspace=None):
@@ -136,29 +145,34 @@ class HHRPagedCache:
         a new tensor of dtype if None) and lse (float32 [B, q_heads], optional).
         scale: 1/sqrt(head_dim) if None.  workspace (new_workspace): needed by calls that may
         run at the same time as another one on this cache."""
-        d, rows = self._table(table)
-        q_seq = self._rows("q", q, d.Hq)
+        index = self._index
+        desc, rows = self._table(table)
+        q_seq = self._rows("q", q, self._Hq)
         if q.shape[0] != rows:
             raise ValueError(f"q: {q.shape[0]} sequences, table has {rows}")
-        check_tensor("lens", lens, torch.int32, self.device, (rows,))
-        if rows > 1 and lens.stride(0) != 1:
-            raise ValueError("lens has to be contiguous")
+        check_vector("lens", lens, torch.int32, rows, index)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif out.shape != q.shape or out.dtype not in (self.dtype, torch.float32) or out.device != self.device or \
-                not out.is_contiguous():
+            out = q.new_empty(q.shape)
+        elif out.shape != q.shape or (out.dtype is not self.dtype and out.dtype is not torch.float32) or \
+                out.get_device() != index or not out.is_contiguous():
             raise ValueError(f"out: expected a contiguous {self.dtype} or float32 tensor {tuple(q.shape)} on {self.device}")
-        if lse is not None:
-            check_tensor("lse", lse, torch.float32, self.device, (rows, d.Hq))
-            if not lse.is_contiguous():
-                raise ValueError("lse has to be contiguous")
-        on_device(self.device, B.hhr_paged_attend, d, rows, q, q_seq, self.K, self.V, table, lens, window,
-                  self.scale if scale is None else scale, _TYPES[out.dtype], out, lse, self.workspace if workspace is None else workspace, None)
+        if lse is not None and (lse.dtype is not torch.float32 or lse.dim() != 2 or lse.shape[0] != rows or
+                                lse.shape[1] != self._Hq or lse.get_device() != index or not lse.is_contiguous()):
+            raise ValueError(f"lse: expected a contiguous float32 tensor [{rows}, {self._Hq}] on {self.device}")
+        if workspace is None:
+            workspace = self.workspace
+        elif workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on {self.device}")
+        st = on_device(index, B.lib().hhr_paged_attend, desc, rows, q.data_ptr(), q_seq, self.K.data_ptr(), self.V.data_ptr(),
+                       table.data_ptr(), lens.data_ptr(), window, self.scale if scale is None else scale, _TYPES[out.dtype],
+                       out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                       workspace.numel() * workspace.element_size())
+        if st:
+            raise B.HhrError(st, "hhr_paged_attend")
         return out
 
     def status(self, stream=None, workspace=None) -> int:
         """HHR_OK, or HHR_ERR_BAD_INDEX after a page, sequence or length out of range; cleared after reading."""
         ws = self.workspace if workspace is None else workspace
-        if stream is not None:
+        with torch.cuda.device(self.device):
             return B.hhr_read_status(ws, stream)
-        return on_device(self.device, B.hhr_read_status, ws)

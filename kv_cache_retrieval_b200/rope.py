@@ -1,6 +1,8 @@
 """Rotary positions on torch tensors: frequencies and the differentiable rotation."""
 from __future__ import annotations
 
+import ctypes as C
+
 import torch
 
 from . import _binding as B
@@ -23,49 +25,65 @@ def rope_freqs(rot, base=10000.0, scaling="none", factor=1.0, orig=0, low=None, 
     return torch.tensor(f, dtype=torch.float64, device=device), mscale
 
 
-def on_device(device, fn, *args):
-    """fn(*args, stream) with `device` current and torch's current stream of it."""
-    if device.type != "cuda":
-        raise ValueError(f"the buffers are on {device}: the library's kernels need a CUDA device")
-    index = device.index
+def on_device(index, fn, *args):
+    """Status of fn(*args, stream) on CUDA device `index` with torch's current stream of it."""
+    if index < 0:
+        raise ValueError("the buffers are not on a CUDA device: the library's kernels need one")
     if index == torch.cuda.current_device():
-        return fn(*args, torch.cuda.current_stream(index).cuda_stream)
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(index):
-        return fn(*args, torch.cuda.current_stream(index).cuda_stream)
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
-def check_tensor(name, t, dtype, device, shape=None):
-    if t.dtype != dtype or t.device != device or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape) if shape is not None else ''} on {device}, "
+def check_vector(name, t, dtype, length, index):
+    """t: contiguous [length] of dtype on CUDA device `index`."""
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != length or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} [{length}] on cuda:{index}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _rotate(x, positions, freqs, interleaved, mscale, transpose, out):
+_rotations = {}
+
+
+def rotation(rot, flags, mscale):
+    """A reference to an hhr_rotation (kept: the few a program uses are made once)."""
+    r = _rotations.get((rot, flags, mscale))
+    if r is None:
+        if len(_rotations) >= 64:
+            _rotations.clear()
+        r = _rotations[rot, flags, mscale] = C.byref(B.hhr_rotation(rot, flags, mscale))
+    return r
+
+
+def _rotate(x, positions, freqs, flags, mscale, out):
     T, H, d = x.shape
-    rot = B.hhr_rotation(2 * freqs.numel(), (B.HHR_ROPE_INTERLEAVED if interleaved else 0) |
-                         (B.HHR_ROPE_TRANSPOSE if transpose else 0), mscale)
-    if x.stride(2) != 1 and d > 1:
+    sx, so = x.stride(), out.stride()
+    if sx[2] != 1 and d > 1:
         x = x.contiguous()
-    on_device(x.device, B.hhr_rope, T, H, d, _TYPES[x.dtype], rot, freqs, positions, x, x.stride(0), x.stride(1),
-              out, out.stride(0), out.stride(1))
+        sx = x.stride()
+    st = on_device(x.get_device(), B.lib().hhr_rope, T, H, d, _TYPES[x.dtype], rotation(2 * freqs.shape[0], flags, mscale),
+                   freqs.data_ptr(), positions.data_ptr(), x.data_ptr(), sx[0], sx[1], out.data_ptr(), so[0], so[1])
+    if st:
+        raise B.HhrError(st, "hhr_rope")
     return out
 
 
 class _Rope(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, positions, freqs, interleaved, mscale):
+    def forward(ctx, x, positions, freqs, flags, mscale):
         ctx.save_for_backward(positions, freqs)
-        ctx.interleaved, ctx.mscale = interleaved, mscale
-        return _rotate(x, positions, freqs, interleaved, mscale, False,
-                       torch.empty(x.shape, dtype=x.dtype, device=x.device))
+        ctx.how = flags, mscale
+        return _rotate(x, positions, freqs, flags, mscale, x.new_empty(x.shape))
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, g):
-        # the Jacobian of a rotation is the rotation: its transpose gives the gradient
+        # the Jacobian of a rotation is the rotation: its transpose gives the gradient, and the gradient's gradient again
         positions, freqs = ctx.saved_tensors
-        return _rotate(g, positions, freqs, ctx.interleaved, ctx.mscale, True,
-                       torch.empty(g.shape, dtype=g.dtype, device=g.device)), None, None, None, None
+        flags, mscale = ctx.how
+        flags ^= B.HHR_ROPE_TRANSPOSE
+        if g.requires_grad and torch.is_grad_enabled():
+            return _Rope.apply(g, positions, freqs, flags, mscale), None, None, None, None
+        return _rotate(g, positions, freqs, flags, mscale, g.new_empty(g.shape)), None, None, None, None
 
 
 def rope(x, positions, freqs, *, interleaved=False, mscale=1.0, out=None):
@@ -74,18 +92,18 @@ def rope(x, positions, freqs, *, interleaved=False, mscale=1.0, out=None):
     with respect to x.  out: where to put the result (x itself rotates in place); not with a gradient."""
     if x.dim() != 3 or x.dtype not in _TYPES or not x.is_cuda:
         raise ValueError(f"x: expected a bf16, fp16 or fp32 CUDA tensor [T, H, d], got {x.dtype} {tuple(x.shape)} on {x.device}")
-    check_tensor("positions", positions, torch.int32, x.device, (x.shape[0],))
-    check_tensor("freqs", freqs, torch.float64, x.device, (freqs.numel(),))
-    if not positions.is_contiguous() or not freqs.is_contiguous():
-        raise ValueError("positions and freqs have to be contiguous")
+    index = x.get_device()
+    check_vector("positions", positions, torch.int32, x.shape[0], index)
+    check_vector("freqs", freqs, torch.float64, freqs.numel(), index)
+    flags = B.HHR_ROPE_INTERLEAVED if interleaved else 0
     if x.requires_grad and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out= has no gradient: call without it, or on x.detach()")
-        return _Rope.apply(x, positions, freqs, interleaved, mscale)
+        return _Rope.apply(x, positions, freqs, flags, mscale)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    else:
-        check_tensor("out", out, x.dtype, x.device, x.shape)
-        if out.stride(2) != 1 and x.shape[2] > 1:
-            raise ValueError("out: the elements of a head have to be adjacent")
-    return _rotate(x, positions, freqs, interleaved, mscale, False, out)
+        out = x.new_empty(x.shape)
+    elif out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != index or \
+            (out.stride(2) != 1 and x.shape[2] > 1):
+        raise ValueError(f"out: expected {x.dtype} {tuple(x.shape)} on {x.device} with adjacent elements of a head, "
+                         f"got {out.dtype} {tuple(out.shape)} on {out.device}")
+    return _rotate(x, positions, freqs, flags, mscale, out)

@@ -265,17 +265,25 @@ def test_gradient_of_a_broadcast_input_and_an_expanded_gradient():
 
 
 @pytest.mark.gpu
-def test_out_has_no_gradient_and_second_derivatives_are_refused():
+def test_out_has_no_gradient():
     x, f = _x((2, 2, 64), torch.float32).requires_grad_(), _freqs(64)
     pos = torch.zeros(2, dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError):
         hhr.rope(x, pos, f, out=torch.empty_like(x))
     with torch.no_grad():
         hhr.rope(x, pos, f, out=torch.empty_like(x))
-    g = torch.ones(2, 2, 64, device="cuda", requires_grad=True)
-    (dx,) = torch.autograd.grad(hhr.rope(x, pos, f), x, g, create_graph=True)
-    with pytest.raises(RuntimeError):
-        dx.sum().backward()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_second_derivative(interleaved):
+    """The gradient is linear in the incoming one: its gradient for it is the rotation."""
+    x, f = _x((5, 2, 64), torch.float32).requires_grad_(), _freqs(48)
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")
+    g, h = _x((5, 2, 64), torch.float32, 1).requires_grad_(), _x((5, 2, 64), torch.float32, 2)
+    (dx,) = torch.autograd.grad(hhr.rope(x, pos, f, interleaved=interleaved), x, g, create_graph=True)
+    (dg,) = torch.autograd.grad(dx, g, h)
+    check(dg, h, pos, f, interleaved=interleaved)
 
 
 # ---------------------------------------------------------------- streams and graphs
