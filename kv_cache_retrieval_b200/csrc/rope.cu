@@ -5,11 +5,11 @@
 //
 // Both calls are one pass over memory: each element is read once and written
 // once, a handful of float32 operations in between, so the bound is HBM (and
-// the launch for a few tokens).  A thread owns one place in a head (2V
-// elements: V pairs, or 2V copied ones) and walks over (token, head) rows with
-// it, so its share of the angle table is read per row from shared memory; the
-// table of the block's tokens is computed once per block, which divides the
-// cost of the float64 angle and of sincospi by the number of heads.
+// the launch for a few tokens).  A block takes whole tokens; a thread owns one
+// place in a head (2V elements: V pairs, or 2V copied ones) and U heads of one
+// token with it, whose pairs turn by the same V angles.  The angles of the
+// block's tokens are computed once, for all of their heads, while the rows
+// are on their way.
 //
 // The angle: pos * f in turns is formed in float64 (an int32 position times a
 // float64 frequency keeps 2^-53 relative, 1e-9 turns at 2^23 turns), reduced
@@ -53,10 +53,10 @@ struct RopeArgs {
   float mscale;
   int T, d, rot, interleaved;
   float sign;                  // -1 for the transposed rotation
-  int heads;                   // H + 2 Hkv rows per token
-  int rows_block;              // (token, head) rows per block
-  int tokens_block;            // most tokens that a block's rows touch
   int places;                  // d / (2V) places of a head
+  int q_groups, kv_groups, groups;   // groups of heads: of queries, of keys (and of values), of a token
+  int tokens_block;            // tokens of a block
+  int split;                   // blocks of a token where one does not hold its groups
 };
 
 template <typename T, int V>
@@ -80,78 +80,79 @@ __device__ __forceinline__ int angle_at(int t, int half, int turns, int place, i
   return V == 1 ? 2 * (t * half + place) : 2 * t * half + ((e >> 1) * turns + place) * 4 + (e & 1) * 2;
 }
 
-// TI: type of x, y, k, v; TC: cache type; V: elements per access; U: rows a
-// thread has in flight.
-template <typename TI, typename TC, int V, int U>
+// TI: type of x, y, k, v; TC: cache type; V: elements per access; U: heads of a token that a thread takes; kCache: keys
+// and values go to a cache.
+template <typename TI, typename TC, int V, int U, bool kCache>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int half = a.rot >> 1;
-  float* cs = reinterpret_cast<float*>(smem);                             // [tokens_block][half] (cos, sin), see angle_at
+  float* cs = reinterpret_cast<float*>(smem);                             // (cos, sin) of the block's tokens, see angle_at
   int64_t* slot = reinterpret_cast<int64_t*>(cs + static_cast<size_t>(a.tokens_block) * a.rot);  // K offset, V offset
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows_block;
-  const int64_t rows_all = static_cast<int64_t>(a.T) * a.heads;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(a.rows_block), rows_all - row0));
-  const int tok0 = static_cast<int>(static_cast<uint32_t>(row0) / static_cast<uint32_t>(a.heads));
-  const int tok_n = static_cast<int>(static_cast<uint32_t>(row0 + rows - 1) / static_cast<uint32_t>(a.heads)) - tok0 + 1;
-
   const int I = a.places;
-  const int place = threadIdx.x % I, first = threadIdx.x / I;
-  const bool idle = first >= kRopeThreads / I;
+  const int place = threadIdx.x % I, unit = threadIdx.x / I;
   const bool turned = place * 2 * V < a.rot;
   // element places of the two halves of this thread's 2V elements
   const int p0 = turned && !a.interleaved ? place * V : place * 2 * V;
   const int p1 = turned && !a.interleaved ? half + place * V : place * 2 * V + V;
   const int turns = half / V;   // places that are turned
 
+  // the block's tokens and this thread's token and group of U heads: queries, then keys, then values
+  int tok0, tok_n, t, group;
+  if (a.split == 1) {
+    tok0 = blockIdx.x * a.tokens_block;
+    tok_n = min(a.tokens_block, a.T - tok0);
+    t = unit / a.groups;
+    group = unit - t * a.groups;
+  } else {
+    tok0 = blockIdx.x / a.split;
+    tok_n = 1;
+    t = 0;
+    group = (blockIdx.x - tok0 * a.split) * (kRopeThreads / I) + unit;
+  }
+  const bool idle = t >= tok_n || group >= a.groups || unit >= kRopeThreads / I;
+  const int64_t tok = tok0 + t;
+  int kind = 0, head = group * U, heads = a.H;
+  if (kCache && group >= a.q_groups) {
+    kind = group >= a.q_groups + a.kv_groups ? 2 : 1;
+    head = (group - a.q_groups - (kind == 2 ? a.kv_groups : 0)) * U;
+    heads = a.Hkv;
+  }
+  const int n = idle || (kind == 0 && !turned && !a.tail) ? 0 : min(U, heads - head);
+
   dependency_wait();
   launch_dependents();
 
-  // this thread's rows: U heads in a row, mostly of one token, all asked for before the angles are computed
-  Pack<TI, V> x0[U], x1[U];
-  int tok[U], head[U];
-  bool live[U];
-  {
-    uint32_t row = static_cast<uint32_t>(row0) + static_cast<uint32_t>(min(first * U, rows - 1));
-    int t = static_cast<int>(row / static_cast<uint32_t>(a.heads));
-    int h = static_cast<int>(row - static_cast<uint32_t>(t) * static_cast<uint32_t>(a.heads));
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      tok[u] = t;
-      head[u] = h;
-      live[u] = !idle && first * U + u < rows && (h >= a.H || turned || a.tail);
-      if (live[u]) {
-        const TI* p;
-        if (h < a.H)
-          p = static_cast<const TI*>(a.x) + t * a.x_tok + h * a.x_head;
-        else if (h < a.H + a.Hkv)
-          p = static_cast<const TI*>(a.k) + t * a.k_row + static_cast<int64_t>(h - a.H) * a.d;
-        else
-          p = static_cast<const TI*>(a.v) + t * a.v_row + static_cast<int64_t>(h - a.H - a.Hkv) * a.d;
-        load<TI, V>(p + p0, x0[u]);
-        load<TI, V>(p + p1, x1[u]);
-      }
-      if (++h == a.heads) {
-        h = 0;
-        ++t;
-      }
-    }
+  // this thread's rows are asked for before the angles are computed
+  const TI* src = static_cast<const TI*>(a.x) + tok * a.x_tok + head * a.x_head;
+  int64_t step = a.x_head;
+  if (kCache && kind) {
+    src = (kind == 1 ? static_cast<const TI*>(a.k) + tok * a.k_row : static_cast<const TI*>(a.v) + tok * a.v_row) +
+          static_cast<int64_t>(head) * a.d;
+    step = a.d;
   }
+  Pack<TI, V> x0[U], x1[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < n) {
+      load<TI, V>(src + u * step + p0, x0[u]);
+      load<TI, V>(src + u * step + p1, x1[u]);
+    }
 
   // the angles of the block's tokens
   for (int i = threadIdx.x; i < tok_n * half; i += kRopeThreads) {
-    const int t = i / half, j = i - t * half;
-    const int p = (a.rope_pos ? a.rope_pos : a.pos)[tok0 + t];
+    const int ti = i / half, j = i - ti * half;
+    const int p = (a.rope_pos ? a.rope_pos : a.pos)[tok0 + ti];
     const double turn = static_cast<double>(p) * a.freqs[j] * 0.15915494309189533577;
     const float r = static_cast<float>(2.0 * (turn - rint(turn)));
     float s, c;
     sincospif(r, &s, &c);
-    *reinterpret_cast<float2*>(cs + angle_at<V>(t, half, turns, j / V, j % V)) = make_float2(a.mscale * c, a.sign * a.mscale * s);
+    *reinterpret_cast<float2*>(cs + angle_at<V>(ti, half, turns, j / V, j % V)) = make_float2(a.mscale * c, a.sign * a.mscale * s);
   }
   // the places of the block's tokens in the cache: element offsets of K and V,
   // or -1 for a token that is not written
-  if (a.Hkv) {
-    for (int t = threadIdx.x; t < tok_n; t += kRopeThreads) {
-      const int tok = tok0 + t, p = a.pos[tok], s = a.seq ? a.seq[tok] : tok;
+  if (kCache) {
+    for (int ti = threadIdx.x; ti < tok_n; ti += kRopeThreads) {
+      const int row = tok0 + ti, p = a.pos[row], s = a.seq ? a.seq[row] : row;
       int64_t ko = -1, vo = -1;
       if (p >= 0) {
         const int col = p / a.page;
@@ -164,121 +165,131 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
           *a.status = HHR_ERR_BAD_INDEX;
         }
       }
-      slot[2 * t] = ko;
-      slot[2 * t + 1] = vo;
+      slot[2 * ti] = ko;
+      slot[2 * ti + 1] = vo;
     }
   }
   __syncthreads();
+  if (n <= 0 || (kCache && slot[2 * t] < 0)) return;
 
-  float w[2 * V];       // cosines and sines of this place, of token `have`
-  int have = -1;
+  TI* yq = static_cast<TI*>(a.y) + tok * a.y_tok + head * a.y_head;
+  if (kind == 2 || !turned) {
+    if (!kCache || kind == 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < n) {
+          *reinterpret_cast<Pack<TI, V>*>(yq + u * a.y_head + p0) = x0[u];
+          *reinterpret_cast<Pack<TI, V>*>(yq + u * a.y_head + p1) = x1[u];
+        }
+    } else {
+      TC* const yc = kind == 2 ? static_cast<TC*>(a.V) + slot[2 * t + 1] + head * a.v_head
+                               : static_cast<TC*>(a.K) + slot[2 * t] + head * a.k_head;
+      const int64_t out_step = kind == 2 ? a.v_head : a.k_head;
+      const float mul = kind == 2 ? a.v_inv : a.k_inv;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < n) {
+          if constexpr (sizeof(TC) == sizeof(TI)) {   // the same type: the bits as they are
+            *reinterpret_cast<Pack<TI, V>*>(yc + u * out_step + p0) = x0[u];
+            *reinterpret_cast<Pack<TI, V>*>(yc + u * out_step + p1) = x1[u];
+          } else {
+            float f0[V], f1[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              f0[e] = to_f32(x0[u].v[e]);
+              f1[e] = to_f32(x1[u].v[e]);
+            }
+            store<TC, V>(yc + u * out_step + p0, f0, mul);
+            store<TC, V>(yc + u * out_step + p1, f1, mul);
+          }
+        }
+    }
+    return;
+  }
+
+  float w[2 * V];       // cosines and sines of this place
+  if constexpr (V == 1) {
+    const float2 z = *reinterpret_cast<const float2*>(cs + angle_at<V>(t, half, turns, place, 0));
+    w[0] = z.x;
+    w[1] = z.y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const float4 z = *reinterpret_cast<const float4*>(cs + angle_at<V>(t, half, turns, place, e));
+      w[2 * e] = z.x;
+      w[2 * e + 1] = z.y;
+      w[2 * e + 2] = z.z;
+      w[2 * e + 3] = z.w;
+    }
+  }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int t = tok[u] - tok0;
-    if (!live[u] || (a.Hkv && slot[2 * t] < 0)) continue;
-    const bool is_q = head[u] < a.H, is_v = head[u] >= a.H + a.Hkv;
-    TI* yq = static_cast<TI*>(a.y) + tok[u] * a.y_tok + head[u] * a.y_head;
-    TC* yc = is_v ? static_cast<TC*>(a.V) + slot[2 * t + 1] + (head[u] - a.H - a.Hkv) * a.v_head
-                  : static_cast<TC*>(a.K) + slot[2 * t] + (head[u] - a.H) * a.k_head;
-    if (is_v || !turned) {
-      if (is_q) {
-        *reinterpret_cast<Pack<TI, V>*>(yq + p0) = x0[u];
-        *reinterpret_cast<Pack<TI, V>*>(yq + p1) = x1[u];
-      } else if constexpr (sizeof(TC) == sizeof(TI)) {   // the same type: the bits as they are
-        *reinterpret_cast<Pack<TI, V>*>(yc + p0) = x0[u];
-        *reinterpret_cast<Pack<TI, V>*>(yc + p1) = x1[u];
-      }
-      if constexpr (sizeof(TC) != sizeof(TI)) {
-        if (!is_q) {
-          float f0[V], f1[V];
+    if (u >= n) break;
+    // halves: pair e is (f0[e], f1[e]); interleaved: (f[2e], f[2e + 1]) of the 2V elements in a row
+    float f[2 * V];
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            f0[e] = to_f32(x0[u].v[e]);
-            f1[e] = to_f32(x1[u].v[e]);
-          }
-          store<TC, V>(yc + p0, f0, is_v ? a.v_inv : a.k_inv);
-          store<TC, V>(yc + p1, f1, is_v ? a.v_inv : a.k_inv);
-        }
-      }
-      continue;
+    for (int e = 0; e < V; ++e) {
+      f[e] = to_f32(x0[u].v[e]);
+      f[V + e] = to_f32(x1[u].v[e]);
     }
-    if (have != t) {
-      have = t;
-      if constexpr (V == 1) {
-        const float2 z = *reinterpret_cast<const float2*>(cs + angle_at<V>(t, half, turns, place, 0));
-        w[0] = z.x;
-        w[1] = z.y;
-      } else {
+    if (a.interleaved) {
 #pragma unroll
-        for (int e = 0; e < V; e += 2) {
-          const float4 z = *reinterpret_cast<const float4*>(cs + angle_at<V>(t, half, turns, place, e));
-          w[2 * e] = z.x;
-          w[2 * e + 1] = z.y;
-          w[2 * e + 2] = z.z;
-          w[2 * e + 3] = z.w;
-        }
+      for (int e = 0; e < V; ++e) {
+        const float u1 = f[2 * e], u2 = f[2 * e + 1];
+        f[2 * e] = fmaf(u1, w[2 * e], -(u2 * w[2 * e + 1]));
+        f[2 * e + 1] = fmaf(u2, w[2 * e], u1 * w[2 * e + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float u1 = f[e], u2 = f[V + e];
+        f[e] = fmaf(u1, w[2 * e], -(u2 * w[2 * e + 1]));
+        f[V + e] = fmaf(u2, w[2 * e], u1 * w[2 * e + 1]);
       }
     }
     float f0[V], f1[V];
-    if (a.interleaved) {
-      float g[2 * V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        g[e] = to_f32(x0[u].v[e]);
-        g[V + e] = to_f32(x1[u].v[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float u1 = g[2 * e], u2 = g[2 * e + 1];
-        g[2 * e] = fmaf(u1, w[2 * e], -(u2 * w[2 * e + 1]));
-        g[2 * e + 1] = fmaf(u2, w[2 * e], u1 * w[2 * e + 1]);
-      }
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        f0[e] = g[e];
-        f1[e] = g[V + e];
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float u1 = to_f32(x0[u].v[e]), u2 = to_f32(x1[u].v[e]);
-        f0[e] = fmaf(u1, w[2 * e], -(u2 * w[2 * e + 1]));
-        f1[e] = fmaf(u2, w[2 * e], u1 * w[2 * e + 1]);
-      }
+    for (int e = 0; e < V; ++e) {
+      f0[e] = f[e];
+      f1[e] = f[V + e];
     }
-    if (is_q) {
-      store<TI, V>(yq + p0, f0, 1.0f);
-      store<TI, V>(yq + p1, f1, 1.0f);
+    if (!kCache || kind == 0) {
+      store<TI, V>(yq + u * a.y_head + p0, f0, 1.0f);
+      store<TI, V>(yq + u * a.y_head + p1, f1, 1.0f);
     } else {
+      TC* const yc = static_cast<TC*>(a.K) + slot[2 * t] + (head + u) * a.k_head;
       store<TC, V>(yc + p0, f0, a.k_inv);
       store<TC, V>(yc + p1, f1, a.k_inv);
     }
   }
 }
 
-// The accesses of a launch are 16 bytes wide where every row, and every place
-// in a row, starts on 16 bytes (8 on the 8-bit side of an append); otherwise
-// they go element by element.
-template <typename TI, typename TC, int V>
+// The accesses of a launch are 16 bytes wide where every row, and every place in a row, starts on 16 bytes (8 on the
+// 8-bit side of an append); otherwise they go element by element.  A thread takes four heads of a token where that still
+// leaves four blocks an SM (8192 tokens x 40 heads: one head 70 us, four 38 us; 8 tokens: 2.2 and 2.0 us for one).
+template <typename TI, typename TC, int V, bool kCache>
 cudaError_t launch_rows(RopeArgs& a, cudaStream_t stream) {
   a.places = a.d / (2 * V);
-  const int step = kRopeThreads / a.places;
-  const int64_t rows = static_cast<int64_t>(a.T) * a.heads;
-  const int U = rows >= static_cast<int64_t>(step) * 4 * 592 ? 4 : 1;
-  a.rows_block = step * U;
-  a.tokens_block = std::min(a.rows_block, (a.rows_block - 2) / a.heads + 2);
-  const size_t smem = static_cast<size_t>(a.tokens_block) * ((a.rot >> 1) * sizeof(float2) + 2 * sizeof(int64_t));
-  const dim3 grid(static_cast<unsigned>((rows + a.rows_block - 1) / a.rows_block));
-  static std::atomic<size_t> raised[2][kMaxDevices];
-  auto kern = U == 4 ? rope_kernel<TI, TC, V, 4> : rope_kernel<TI, TC, V, 1>;
-  if (smem > 48 * 1024)
-    if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem, raised[U == 4])) return e;
-  return launch_dependent<RopeArgs>(kern, grid, kRopeThreads, smem, stream, a);
+  const int step = kRopeThreads / a.places;      // groups of a block
+  const int64_t rows = static_cast<int64_t>(a.T) * (a.H + 2 * a.Hkv);
+  const int U = a.H + 2 * a.Hkv >= 4 && rows >= static_cast<int64_t>(step) * 4 * 592 ? 4 : 1;
+  a.q_groups = (a.H + U - 1) / U;
+  a.kv_groups = (a.Hkv + U - 1) / U;
+  a.groups = a.q_groups + 2 * a.kv_groups;
+  // whole tokens in a block, or several blocks of a token
+  a.tokens_block = std::max(1, step / a.groups);
+  a.split = a.groups > step ? (a.groups + step - 1) / step : 1;
+  const size_t smem = static_cast<size_t>(a.tokens_block) * (a.rot * sizeof(float) + 2 * sizeof(int64_t));
+  const int64_t blocks = a.split > 1 ? static_cast<int64_t>(a.T) * a.split : (a.T + a.tokens_block - 1) / a.tokens_block;
+  if (blocks >= int64_t{1} << 31) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks));
+  return U == 4 ? launch_dependent<RopeArgs>(rope_kernel<TI, TC, V, 4, kCache>, grid, kRopeThreads, smem, stream, a)
+                : launch_dependent<RopeArgs>(rope_kernel<TI, TC, V, 1, kCache>, grid, kRopeThreads, smem, stream, a);
 }
 
-template <typename TI, typename TC>
+template <typename TI, typename TC, bool kCache>
 cudaError_t launch_typed(RopeArgs& a, bool wide, cudaStream_t stream) {
-  return wide ? launch_rows<TI, TC, 16 / sizeof(TI)>(a, stream) : launch_rows<TI, TC, 1>(a, stream);
+  return wide ? launch_rows<TI, TC, 16 / sizeof(TI), kCache>(a, stream) : launch_rows<TI, TC, 1, kCache>(a, stream);
 }
 
 int32_t check_rotation(const hhr_rotation* r, const double* freqs, int d) {
@@ -366,7 +377,7 @@ int32_t hhr_rope(int32_t T, int32_t H, int32_t d, int32_t type, const hhr_rotati
   a.x_head = x_head;
   a.y_tok = y_tok;
   a.y_head = y_head;
-  a.H = a.heads = H;
+  a.H = H;
   a.tail = x != y;
   a.pos = pos;
   a.freqs = freqs;
@@ -380,9 +391,9 @@ int32_t hhr_rope(int32_t T, int32_t H, int32_t d, int32_t type, const hhr_rotati
   const bool wide = d % unit == 0 && a.rot % unit == 0 && wide_row(x, x_tok, x_head, size) && wide_row(y, y_tok, y_head, size);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (type) {
-    case HHR_TYPE_BF16: return status_of(launch_typed<__nv_bfloat16, __nv_bfloat16>(a, wide, s));
-    case HHR_TYPE_F16: return status_of(launch_typed<__half, __half>(a, wide, s));
-    default: return status_of(launch_typed<float, float>(a, wide, s));
+    case HHR_TYPE_BF16: return status_of(launch_typed<__nv_bfloat16, __nv_bfloat16, false>(a, wide, s));
+    case HHR_TYPE_F16: return status_of(launch_typed<__half, __half, false>(a, wide, s));
+    default: return status_of(launch_typed<float, float, false>(a, wide, s));
   }
 }
 
@@ -451,15 +462,14 @@ int32_t hhr_paged_append(const hhr_paged* cache, int32_t T, int32_t B,
   a.T = T;
   a.d = c.d;
   a.rot = rotation ? rotation->rot : 0;
-  a.heads = a.H + 2 * c.Hkv;
   const bool wide = a.rot % 16 == 0 && wide_row(k, k_row, 0, 2) && wide_row(v, v_row, 0, 2) &&
                     (!q || (wide_row(q, q_tok, 0, 2) && wide_row(q_out, q_out_tok, 0, 2)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = c.kv_type == HHR_TYPE_E4M3;
   if (c.q_type == HHR_TYPE_BF16)
-    return status_of(e4m3 ? launch_typed<__nv_bfloat16, __nv_fp8_e4m3>(a, wide, s)
-                          : launch_typed<__nv_bfloat16, __nv_bfloat16>(a, wide, s));
-  return status_of(e4m3 ? launch_typed<__half, __nv_fp8_e4m3>(a, wide, s) : launch_typed<__half, __half>(a, wide, s));
+    return status_of(e4m3 ? launch_typed<__nv_bfloat16, __nv_fp8_e4m3, true>(a, wide, s)
+                          : launch_typed<__nv_bfloat16, __nv_bfloat16, true>(a, wide, s));
+  return status_of(e4m3 ? launch_typed<__half, __nv_fp8_e4m3, true>(a, wide, s) : launch_typed<__half, __half, true>(a, wide, s));
 }
 
 }  // extern "C"
