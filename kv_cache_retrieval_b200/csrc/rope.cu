@@ -5,7 +5,7 @@
 //
 // Both calls are one pass over memory: each element is read once and written
 // once, a handful of float32 operations in between, so the bound is HBM (and
-// the launch for a few tokens).  A block takes whole tokens; a thread owns one
+// the launch for a few tokens).  A thread owns one
 // place in a head (2V elements: V pairs, or 2V copied ones) and U heads of one
 // token with it, whose pairs turn by the same V angles.  The angles of the
 // block's tokens are computed once, for all of their heads, while the rows
@@ -55,8 +55,8 @@ struct RopeArgs {
   float sign;                  // -1 for the transposed rotation
   int places;                  // d / (2V) places of a head
   int q_groups, kv_groups, groups;   // groups of heads: of queries, of keys (and of values), of a token
-  int tokens_block;            // tokens of a block
-  int split;                   // blocks of a token where one does not hold its groups
+  int units, tiles;            // (token, group) pairs, and tiles of as many as a block has rows of threads
+  int tokens_block;            // most tokens that a tile touches
 };
 
 template <typename T, int V>
@@ -80,187 +80,251 @@ __device__ __forceinline__ int angle_at(int t, int half, int turns, int place, i
   return V == 1 ? 2 * (t * half + place) : 2 * t * half + ((e >> 1) * turns + place) * 4 + (e & 1) * 2;
 }
 
+// What a thread has of a tile (as many (token, group of U heads) as a block has rows of threads).
+struct RopePart {
+  int tok0, tok_n;   // the tile's tokens
+  int t;             // the thread's token of these
+  int kind;          // 0 queries, 1 keys, 2 values
+  int head, n;       // its first head and how many
+};
+
 // TI: type of x, y, k, v; TC: cache type; V: elements per access; U: heads of a token that a thread takes; kCache: keys
 // and values go to a cache.
 template <typename TI, typename TC, int V, int U, bool kCache>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+  constexpr bool kStaged = V > 1;      // rows come through shared memory, a tile ahead
   extern __shared__ __align__(16) unsigned char smem[];
   const int half = a.rot >> 1;
-  float* cs = reinterpret_cast<float*>(smem);                             // (cos, sin) of the block's tokens, see angle_at
-  int64_t* slot = reinterpret_cast<int64_t*>(cs + static_cast<size_t>(a.tokens_block) * a.rot);  // K offset, V offset
+  // two tiles' rows, [2][U][2][threads] accesses; two tiles' (cos, sin), see angle_at; their K and V offsets
+  Pack<TI, V>* const rows = reinterpret_cast<Pack<TI, V>*>(smem);
+  float* const cs_all = reinterpret_cast<float*>(smem + (kStaged ? 2 * U * 2 * kRopeThreads * 16 : 0));
+  int64_t* const slot_all = reinterpret_cast<int64_t*>(cs_all + 2 * static_cast<size_t>(a.tokens_block) * a.rot);
   const int I = a.places;
   const int place = threadIdx.x % I, unit = threadIdx.x / I;
   const bool turned = place * 2 * V < a.rot;
-  // element places of the two halves of this thread's 2V elements
-  const int p0 = turned && !a.interleaved ? place * V : place * 2 * V;
-  const int p1 = turned && !a.interleaved ? half + place * V : place * 2 * V + V;
   const int turns = half / V;   // places that are turned
+  // This thread's 2V elements: V in the first half of the turned (or of the copied) elements and V in the second, so
+  // that neighbouring threads' accesses are adjacent; an access of more than one element holds whole interleaved pairs.
+  int p0 = place * V, p1 = half + place * V;
+  if (V == 1 && a.interleaved) {
+    p0 = 2 * place;
+    p1 = p0 + 1;
+  }
+  if (!turned) {
+    p0 = a.rot + (place - turns) * V;
+    p1 = p0 + (a.d - a.rot) / 2;
+  }
+  const int n_units = kRopeThreads / I;
 
-  // the block's tokens and this thread's token and group of U heads: queries, then keys, then values
-  int tok0, tok_n, t, group;
-  if (a.split == 1) {
-    tok0 = blockIdx.x * a.tokens_block;
-    tok_n = min(a.tokens_block, a.T - tok0);
-    t = unit / a.groups;
-    group = unit - t * a.groups;
-  } else {
-    tok0 = blockIdx.x / a.split;
-    tok_n = 1;
-    t = 0;
-    group = (blockIdx.x - tok0 * a.split) * (kRopeThreads / I) + unit;
-  }
-  const bool idle = t >= tok_n || group >= a.groups || unit >= kRopeThreads / I;
-  const int64_t tok = tok0 + t;
-  int kind = 0, head = group * U, heads = a.H;
-  if (kCache && group >= a.q_groups) {
-    kind = group >= a.q_groups + a.kv_groups ? 2 : 1;
-    head = (group - a.q_groups - (kind == 2 ? a.kv_groups : 0)) * U;
-    heads = a.Hkv;
-  }
-  const int n = idle || (kind == 0 && !turned && !a.tail) ? 0 : min(U, heads - head);
+  const auto part_of = [&](int tile) {   // heads: queries, then keys, then values
+    RopePart w;
+    const int first = tile * n_units, last = min(first + n_units, a.units) - 1;
+    w.tok0 = first / a.groups;
+    w.tok_n = last / a.groups - w.tok0 + 1;
+    const int tok = (first + unit) / a.groups;
+    const int group = first + unit - tok * a.groups;
+    w.t = tok - w.tok0;
+    w.kind = 0;
+    w.head = group * U;
+    int heads = a.H;
+    if (kCache && group >= a.q_groups) {
+      w.kind = group >= a.q_groups + a.kv_groups ? 2 : 1;
+      w.head = (group - a.q_groups - (w.kind == 2 ? a.kv_groups : 0)) * U;
+      heads = a.Hkv;
+    }
+    const bool idle = unit >= n_units || first + unit > last;
+    w.n = idle || (w.kind == 0 && !turned && !a.tail) ? 0 : min(U, heads - w.head);
+    return w;
+  };
+  const auto source = [&](const RopePart& w, int u) {
+    const int64_t tok = w.tok0 + w.t;
+    if (kCache && w.kind)
+      return (w.kind == 1 ? static_cast<const TI*>(a.k) + tok * a.k_row : static_cast<const TI*>(a.v) + tok * a.v_row) +
+             static_cast<int64_t>(w.head + u) * a.d;
+    return static_cast<const TI*>(a.x) + tok * a.x_tok + (w.head + u) * a.x_head;
+  };
+  // A token's place in its sequence and the sequence; the page that the table has for it; the element offsets of K and V
+  // there, or -1 for a token that is not written.
+  const auto place_of = [&](int row) {
+    return row < a.T ? make_int2(a.pos[row], a.seq ? a.seq[row] : row) : make_int2(-1, 0);
+  };
+  const auto page_of = [&](int2 at) {
+    const int col = at.x < 0 ? 0 : at.x / a.page;
+    if (at.x < 0 || at.y < 0 || at.y >= a.B || col >= a.table_cols) return -1;
+    return a.table[static_cast<int64_t>(at.y) * a.table_stride + col];
+  };
+  const auto place_token = [&](int2 at, int id, int64_t* out) {
+    int64_t ko = -1, vo = -1;
+    if (at.x >= 0) {
+      if (id >= 0 && id < a.n_pages) {
+        const int in_page = at.x - at.x / a.page * a.page;
+        ko = id * a.k_page + in_page * a.k_tok;
+        vo = id * a.v_page + in_page * a.v_tok;
+      } else if (a.status) {
+        *a.status = HHR_ERR_BAD_INDEX;
+      }
+    }
+    out[0] = ko;
+    out[1] = vo;
+  };
+  const auto ask = [&](const RopePart& w, int buf) {   // each thread's own rows: no barrier between them and their use
+    if constexpr (kStaged) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < w.n) {
+          const TI* const src = source(w, u);
+          const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(rows + ((buf * U + u) * 2) * kRopeThreads + threadIdx.x));
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src + p0) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + kRopeThreads * 16), "l"(src + p1) : "memory");
+        }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
 
   dependency_wait();
   launch_dependents();
 
-  // this thread's rows are asked for before the angles are computed
-  const TI* src = static_cast<const TI*>(a.x) + tok * a.x_tok + head * a.x_head;
-  int64_t step = a.x_head;
-  if (kCache && kind) {
-    src = (kind == 1 ? static_cast<const TI*>(a.k) + tok * a.k_row : static_cast<const TI*>(a.v) + tok * a.v_row) +
-          static_cast<int64_t>(head) * a.d;
-    step = a.d;
+  int tile = blockIdx.x, buf = 0;
+  RopePart w = part_of(tile);
+  ask(w, 0);
+  // of this thread's token of the tile: its place and page; of the next tile's: its place
+  int2 at = make_int2(-1, 0), at_next = at;
+  int id = -1;
+  const auto token_of = [&](const RopePart& part) { return static_cast<int>(threadIdx.x) < part.tok_n ? part.tok0 + static_cast<int>(threadIdx.x) : a.T; };
+  if (kCache) {
+    at = place_of(token_of(w));
+    if (tile + gridDim.x < a.tiles) at_next = place_of(token_of(part_of(tile + gridDim.x)));
+    id = page_of(at);
   }
-  Pack<TI, V> x0[U], x1[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (u < n) {
-      load<TI, V>(src + u * step + p0, x0[u]);
-      load<TI, V>(src + u * step + p1, x1[u]);
+  while (true) {
+    const int next = tile + gridDim.x;
+    const int tid = threadIdx.x;
+    RopePart w_next = w;
+    if (next < a.tiles) w_next = part_of(next);
+    if (next >= a.tiles) w_next.n = 0;
+    ask(w_next, buf ^ 1);
+
+    // the angles of the tile's tokens, and their places in the cache, whose page was looked up while the tile before
+    // was written
+    float* const cs = cs_all + static_cast<size_t>(buf) * a.tokens_block * a.rot;
+    int64_t* const slot = slot_all + static_cast<size_t>(buf) * a.tokens_block * 2;
+    for (int i = threadIdx.x; i < w.tok_n * half; i += kRopeThreads) {
+      const int ti = i / half, j = i - ti * half;
+      const int p = (a.rope_pos ? a.rope_pos : a.pos)[w.tok0 + ti];
+      const double turn = static_cast<double>(p) * a.freqs[j] * 0.15915494309189533577;
+      const float r = static_cast<float>(2.0 * (turn - rint(turn)));
+      float s, c;
+      sincospif(r, &s, &c);
+      int to = j / V, e = j % V;     // the place that pair j belongs to, and the which-th of its pairs
+      if (V > 1 && a.interleaved) {
+        const int access = 2 * j / V;
+        to = access < turns ? access : access - turns;
+        e = (2 * j - access * V) / 2 + (access < turns ? 0 : V / 2);
+      }
+      *reinterpret_cast<float2*>(cs + angle_at<V>(ti, half, turns, to, e)) =
+          make_float2(a.mscale * c, a.sign * a.mscale * s);
+    }
+    if (kCache && tid < w.tok_n) place_token(at, id, slot + 2 * tid);
+    // (one barrier a tile: the buffers of the tile after next are written behind the next one)
+    __syncthreads();
+    if constexpr (kStaged) asm volatile("cp.async.wait_group 1;" ::: "memory");
+
+    int id_next = -1;
+    int2 at_after = make_int2(-1, 0);
+    if (kCache && next < a.tiles) {
+      id_next = page_of(at_next);
+      if (next + gridDim.x < a.tiles) at_after = place_of(token_of(part_of(next + gridDim.x)));
     }
 
-  // the angles of the block's tokens
-  for (int i = threadIdx.x; i < tok_n * half; i += kRopeThreads) {
-    const int ti = i / half, j = i - ti * half;
-    const int p = (a.rope_pos ? a.rope_pos : a.pos)[tok0 + ti];
-    const double turn = static_cast<double>(p) * a.freqs[j] * 0.15915494309189533577;
-    const float r = static_cast<float>(2.0 * (turn - rint(turn)));
-    float s, c;
-    sincospif(r, &s, &c);
-    *reinterpret_cast<float2*>(cs + angle_at<V>(ti, half, turns, j / V, j % V)) = make_float2(a.mscale * c, a.sign * a.mscale * s);
-  }
-  // the places of the block's tokens in the cache: element offsets of K and V,
-  // or -1 for a token that is not written
-  if (kCache) {
-    for (int ti = threadIdx.x; ti < tok_n; ti += kRopeThreads) {
-      const int row = tok0 + ti, p = a.pos[row], s = a.seq ? a.seq[row] : row;
-      int64_t ko = -1, vo = -1;
-      if (p >= 0) {
-        const int col = p / a.page;
-        int id = -1;
-        if (s >= 0 && s < a.B && col < a.table_cols) id = a.table[static_cast<int64_t>(s) * a.table_stride + col];
-        if (id >= 0 && id < a.n_pages) {
-          ko = id * a.k_page + (p - col * a.page) * a.k_tok;
-          vo = id * a.v_page + (p - col * a.page) * a.v_tok;
-        } else if (a.status) {
-          *a.status = HHR_ERR_BAD_INDEX;
+    const int n = kCache && w.n > 0 && slot[2 * w.t] < 0 ? 0 : w.n;
+    const bool turn = turned && w.kind != 2;
+    float cw[2 * V];       // cosines and sines of this place
+    if (turn && n > 0) {
+      if constexpr (V == 1) {
+        const float2 z = *reinterpret_cast<const float2*>(cs + angle_at<V>(w.t, half, turns, place, 0));
+        cw[0] = z.x;
+        cw[1] = z.y;
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          const float4 z = *reinterpret_cast<const float4*>(cs + angle_at<V>(w.t, half, turns, place, e));
+          cw[2 * e] = z.x;
+          cw[2 * e + 1] = z.y;
+          cw[2 * e + 2] = z.z;
+          cw[2 * e + 3] = z.w;
         }
       }
-      slot[2 * ti] = ko;
-      slot[2 * ti + 1] = vo;
     }
-  }
-  __syncthreads();
-  if (n <= 0 || (kCache && slot[2 * t] < 0)) return;
-
-  TI* yq = static_cast<TI*>(a.y) + tok * a.y_tok + head * a.y_head;
-  if (kind == 2 || !turned) {
-    if (!kCache || kind == 0) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < n) {
-          *reinterpret_cast<Pack<TI, V>*>(yq + u * a.y_head + p0) = x0[u];
-          *reinterpret_cast<Pack<TI, V>*>(yq + u * a.y_head + p1) = x1[u];
-        }
-    } else {
-      TC* const yc = kind == 2 ? static_cast<TC*>(a.V) + slot[2 * t + 1] + head * a.v_head
-                               : static_cast<TC*>(a.K) + slot[2 * t] + head * a.k_head;
-      const int64_t out_step = kind == 2 ? a.v_head : a.k_head;
-      const float mul = kind == 2 ? a.v_inv : a.k_inv;
+    for (int u = 0; u < U; ++u) {
+      if (u >= n) break;
+      Pack<TI, V> x0, x1;
+      if constexpr (kStaged) {
+        x0 = rows[((buf * U + u) * 2) * kRopeThreads + threadIdx.x];
+        x1 = rows[((buf * U + u) * 2 + 1) * kRopeThreads + threadIdx.x];
+      } else {
+        load<TI, V>(source(w, u) + p0, x0);
+        load<TI, V>(source(w, u) + p1, x1);
+      }
+      const int64_t tok = w.tok0 + w.t;
+      const bool is_q = !kCache || w.kind == 0;
+      TI* const yq = static_cast<TI*>(a.y) + tok * a.y_tok + (w.head + u) * a.y_head;
+      TC* yc = nullptr;
+      if (!is_q)
+        yc = w.kind == 2 ? static_cast<TC*>(a.V) + slot[2 * w.t + 1] + (w.head + u) * a.v_head
+                         : static_cast<TC*>(a.K) + slot[2 * w.t] + (w.head + u) * a.k_head;
+      if (!turn && (is_q || sizeof(TC) == sizeof(TI))) {   // the same type: the bits as they are
+        TI* const y = is_q ? yq : reinterpret_cast<TI*>(yc);
+        *reinterpret_cast<Pack<TI, V>*>(y + p0) = x0;
+        *reinterpret_cast<Pack<TI, V>*>(y + p1) = x1;
+        continue;
+      }
+      // halves: pair e is (f[e], f[V + e]); interleaved: (f[2e], f[2e + 1])
+      float f[2 * V];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u < n) {
-          if constexpr (sizeof(TC) == sizeof(TI)) {   // the same type: the bits as they are
-            *reinterpret_cast<Pack<TI, V>*>(yc + u * out_step + p0) = x0[u];
-            *reinterpret_cast<Pack<TI, V>*>(yc + u * out_step + p1) = x1[u];
-          } else {
-            float f0[V], f1[V];
+      for (int e = 0; e < V; ++e) {
+        f[e] = to_f32(x0.v[e]);
+        f[V + e] = to_f32(x1.v[e]);
+      }
+      if (turn) {
+        if (a.interleaved) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-              f0[e] = to_f32(x0[u].v[e]);
-              f1[e] = to_f32(x1[u].v[e]);
-            }
-            store<TC, V>(yc + u * out_step + p0, f0, mul);
-            store<TC, V>(yc + u * out_step + p1, f1, mul);
+          for (int e = 0; e < V; ++e) {
+            const float u1 = f[2 * e], u2 = f[2 * e + 1];
+            f[2 * e] = fmaf(u1, cw[2 * e], -(u2 * cw[2 * e + 1]));
+            f[2 * e + 1] = fmaf(u2, cw[2 * e], u1 * cw[2 * e + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float u1 = f[e], u2 = f[V + e];
+            f[e] = fmaf(u1, cw[2 * e], -(u2 * cw[2 * e + 1]));
+            f[V + e] = fmaf(u2, cw[2 * e], u1 * cw[2 * e + 1]);
           }
         }
-    }
-    return;
-  }
-
-  float w[2 * V];       // cosines and sines of this place
-  if constexpr (V == 1) {
-    const float2 z = *reinterpret_cast<const float2*>(cs + angle_at<V>(t, half, turns, place, 0));
-    w[0] = z.x;
-    w[1] = z.y;
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; e += 2) {
-      const float4 z = *reinterpret_cast<const float4*>(cs + angle_at<V>(t, half, turns, place, e));
-      w[2 * e] = z.x;
-      w[2 * e + 1] = z.y;
-      w[2 * e + 2] = z.z;
-      w[2 * e + 3] = z.w;
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (u >= n) break;
-    // halves: pair e is (f0[e], f1[e]); interleaved: (f[2e], f[2e + 1]) of the 2V elements in a row
-    float f[2 * V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      f[e] = to_f32(x0[u].v[e]);
-      f[V + e] = to_f32(x1[u].v[e]);
-    }
-    if (a.interleaved) {
+      }
+      float f0[V], f1[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float u1 = f[2 * e], u2 = f[2 * e + 1];
-        f[2 * e] = fmaf(u1, w[2 * e], -(u2 * w[2 * e + 1]));
-        f[2 * e + 1] = fmaf(u2, w[2 * e], u1 * w[2 * e + 1]);
+        f0[e] = f[e];
+        f1[e] = f[V + e];
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float u1 = f[e], u2 = f[V + e];
-        f[e] = fmaf(u1, w[2 * e], -(u2 * w[2 * e + 1]));
-        f[V + e] = fmaf(u2, w[2 * e], u1 * w[2 * e + 1]);
+      if (is_q) {
+        store<TI, V>(yq + p0, f0, 1.0f);
+        store<TI, V>(yq + p1, f1, 1.0f);
+      } else {
+        const float mul = w.kind == 2 ? a.v_inv : a.k_inv;
+        store<TC, V>(yc + p0, f0, mul);
+        store<TC, V>(yc + p1, f1, mul);
       }
     }
-    float f0[V], f1[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      f0[e] = f[e];
-      f1[e] = f[V + e];
-    }
-    if (!kCache || kind == 0) {
-      store<TI, V>(yq + u * a.y_head + p0, f0, 1.0f);
-      store<TI, V>(yq + u * a.y_head + p1, f1, 1.0f);
-    } else {
-      TC* const yc = static_cast<TC*>(a.K) + slot[2 * t] + (head + u) * a.k_head;
-      store<TC, V>(yc + p0, f0, a.k_inv);
-      store<TC, V>(yc + p1, f1, a.k_inv);
-    }
+    if (next >= a.tiles) break;
+    tile = next;
+    w = w_next;
+    buf ^= 1;
+    at = at_next;
+    id = id_next;
+    at_next = at_after;
   }
 }
 
@@ -276,15 +340,20 @@ cudaError_t launch_rows(RopeArgs& a, cudaStream_t stream) {
   a.q_groups = (a.H + U - 1) / U;
   a.kv_groups = (a.Hkv + U - 1) / U;
   a.groups = a.q_groups + 2 * a.kv_groups;
-  // whole tokens in a block, or several blocks of a token
-  a.tokens_block = std::max(1, step / a.groups);
-  a.split = a.groups > step ? (a.groups + step - 1) / step : 1;
-  const size_t smem = static_cast<size_t>(a.tokens_block) * (a.rot * sizeof(float) + 2 * sizeof(int64_t));
-  const int64_t blocks = a.split > 1 ? static_cast<int64_t>(a.T) * a.split : (a.T + a.tokens_block - 1) / a.tokens_block;
-  if (blocks >= int64_t{1} << 31) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks));
-  return U == 4 ? launch_dependent<RopeArgs>(rope_kernel<TI, TC, V, 4, kCache>, grid, kRopeThreads, smem, stream, a)
-                : launch_dependent<RopeArgs>(rope_kernel<TI, TC, V, 1, kCache>, grid, kRopeThreads, smem, stream, a);
+  a.units = static_cast<int>(static_cast<int64_t>(a.T) * a.groups);
+  a.tokens_block = std::min(step, (step - 2 + a.groups) / a.groups + 1);
+  a.tiles = (a.units - 1) / step + 1;
+  const size_t smem = (V > 1 ? static_cast<size_t>(2 * U) * 2 * kRopeThreads * 16 : 0) +
+                      2 * static_cast<size_t>(a.tokens_block) * (a.rot * sizeof(float) + 2 * sizeof(int64_t));
+  static std::atomic<size_t> raised[2][kMaxDevices];
+  const auto kern = U == 4 ? rope_kernel<TI, TC, V, 4, kCache> : rope_kernel<TI, TC, V, 1, kCache>;
+  int dev = 0, sms = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return e;
+  if (smem > 48 * 1024)
+    if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem, raised[U == 4])) return e;
+  const dim3 grid(static_cast<unsigned>(std::min(a.tiles, sms * (U == 4 ? 3 : 8))));
+  return launch_dependent<RopeArgs>(kern, grid, kRopeThreads, smem, stream, a);
 }
 
 template <typename TI, typename TC, bool kCache>
