@@ -5,11 +5,9 @@
 //
 // Both calls are one pass over memory: each element is read once and written
 // once, a handful of float32 operations in between, so the bound is HBM (and
-// the launch for a few tokens).  A thread owns one
-// place in a head (2V elements: V pairs, or 2V copied ones) and U heads of one
-// token with it, whose pairs turn by the same V angles.  The angles of the
-// block's tokens are computed once, for all of their heads, while the rows
-// are on their way.
+// the launch for a few tokens).  A thread owns one place in a head (2V elements: V pairs, or 2V copied ones) and U heads of one
+// token with it, whose pairs turn by the same V angles.  The angles of a tile's
+// tokens are computed once, for all of their heads, while rows are on their way.
 //
 // The angle: pos * f in turns is formed in float64 (an int32 position times a
 // float64 frequency keeps 2^-53 relative, 1e-9 turns at 2^23 turns), reduced
@@ -55,7 +53,8 @@ struct RopeArgs {
   float sign;                  // -1 for the transposed rotation
   int places;                  // d / (2V) places of a head
   int q_groups, kv_groups, groups;   // groups of heads: of queries, of keys (and of values), of a token
-  int units, tiles;            // (token, group) pairs, and tiles of as many as a block has rows of threads
+  uint32_t units;
+  int tiles;                   // (token, group) pairs, and tiles of as many as a block has rows of threads
   int tokens_block;            // most tokens that a tile touches
 };
 
@@ -92,7 +91,7 @@ struct RopePart {
 // and values go to a cache.
 template <typename TI, typename TC, int V, int U, bool kCache>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
-  constexpr bool kStaged = V > 1;      // rows come through shared memory, a tile ahead
+  constexpr bool kStaged = V > 1 && U > 1;   // rows come through shared memory, a tile ahead; or else by plain loads
   extern __shared__ __align__(16) unsigned char smem[];
   const int half = a.rot >> 1;
   // two tiles' rows, [2][U][2][threads] accesses; two tiles' (cos, sin), see angle_at; their K and V offsets
@@ -118,11 +117,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
 
   const auto part_of = [&](int tile) {   // heads: queries, then keys, then values
     RopePart w;
-    const int first = tile * n_units, last = min(first + n_units, a.units) - 1;
-    w.tok0 = first / a.groups;
-    w.tok_n = last / a.groups - w.tok0 + 1;
-    const int tok = (first + unit) / a.groups;
-    const int group = first + unit - tok * a.groups;
+    const uint32_t first = static_cast<uint32_t>(tile) * n_units, groups = a.groups;
+    const uint32_t last = first + min(static_cast<uint32_t>(n_units), a.units - first) - 1;
+    w.tok0 = static_cast<int>(first / groups);
+    w.tok_n = static_cast<int>(last / groups) - w.tok0 + 1;
+    const int tok = static_cast<int>((first + unit) / groups);
+    const int group = static_cast<int>(first + unit - tok * groups);
     w.t = tok - w.tok0;
     w.kind = 0;
     w.head = group * U;
@@ -187,18 +187,27 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
   int tile = blockIdx.x, buf = 0;
   RopePart w = part_of(tile);
   ask(w, 0);
+  Pack<TI, V> x0s[U], x1s[U];
+  if constexpr (!kStaged) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (u < w.n) {
+        load<TI, V>(source(w, u) + p0, x0s[u]);
+        load<TI, V>(source(w, u) + p1, x1s[u]);
+      }
+  }
   // of this thread's token of the tile: its place and page; of the next tile's: its place
   int2 at = make_int2(-1, 0), at_next = at;
   int id = -1;
-  const auto token_of = [&](const RopePart& part) { return static_cast<int>(threadIdx.x) < part.tok_n ? part.tok0 + static_cast<int>(threadIdx.x) : a.T; };
-  if (kCache) {
+  const int duty = kRopeThreads - 1 - static_cast<int>(threadIdx.x);   // (the last warps have fewer angles to compute)
+  const auto token_of = [&](const RopePart& part) { return duty < part.tok_n ? part.tok0 + duty : a.T; };
+  if (kCache && duty < a.tokens_block) {
     at = place_of(token_of(w));
-    if (tile + gridDim.x < a.tiles) at_next = place_of(token_of(part_of(tile + gridDim.x)));
+    if (kStaged && tile + gridDim.x < a.tiles) at_next = place_of(token_of(part_of(tile + gridDim.x)));
     id = page_of(at);
   }
   while (true) {
-    const int next = tile + gridDim.x;
-    const int tid = threadIdx.x;
+    const int next = kStaged ? tile + static_cast<int>(gridDim.x) : a.tiles;
     RopePart w_next = w;
     if (next < a.tiles) w_next = part_of(next);
     if (next >= a.tiles) w_next.n = 0;
@@ -224,14 +233,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
       *reinterpret_cast<float2*>(cs + angle_at<V>(ti, half, turns, to, e)) =
           make_float2(a.mscale * c, a.sign * a.mscale * s);
     }
-    if (kCache && tid < w.tok_n) place_token(at, id, slot + 2 * tid);
+    if (kCache && duty < w.tok_n) place_token(at, id, slot + 2 * duty);
     // (one barrier a tile: the buffers of the tile after next are written behind the next one)
     __syncthreads();
     if constexpr (kStaged) asm volatile("cp.async.wait_group 1;" ::: "memory");
 
     int id_next = -1;
     int2 at_after = make_int2(-1, 0);
-    if (kCache && next < a.tiles) {
+    if (kCache && duty < a.tokens_block && next < a.tiles) {
       id_next = page_of(at_next);
       if (next + gridDim.x < a.tiles) at_after = place_of(token_of(part_of(next + gridDim.x)));
     }
@@ -263,8 +272,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
         x0 = rows[((buf * U + u) * 2) * kRopeThreads + threadIdx.x];
         x1 = rows[((buf * U + u) * 2 + 1) * kRopeThreads + threadIdx.x];
       } else {
-        load<TI, V>(source(w, u) + p0, x0);
-        load<TI, V>(source(w, u) + p1, x1);
+        x0 = x0s[u];
+        x1 = x1s[u];
       }
       const int64_t tok = w.tok0 + w.t;
       const bool is_q = !kCache || w.kind == 0;
@@ -329,8 +338,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
 }
 
 // The accesses of a launch are 16 bytes wide where every row, and every place in a row, starts on 16 bytes (8 on the
-// 8-bit side of an append); otherwise they go element by element.  A thread takes four heads of a token where that still
-// leaves four blocks an SM (8192 tokens x 40 heads: one head 70 us, four 38 us; 8 tokens: 2.2 and 2.0 us for one).
+// 8-bit side of an append); otherwise they go element by element.  Few tokens: a thread takes one head by plain loads, a
+// block one tile (8 tokens, 40 heads: 1.7 us, 2.0 staged).  Where four heads a thread still make four blocks an SM:
+// three blocks an SM take the tiles in turn and stage the next one's rows in shared memory (8192 tokens, 40 heads of 128
+// bf16: 58 us with one head a thread, 45 with two, 40 with four, 29 staged; two or four blocks an SM: 35, 33).
 template <typename TI, typename TC, int V, bool kCache>
 cudaError_t launch_rows(RopeArgs& a, cudaStream_t stream) {
   a.places = a.d / (2 * V);
@@ -340,10 +351,10 @@ cudaError_t launch_rows(RopeArgs& a, cudaStream_t stream) {
   a.q_groups = (a.H + U - 1) / U;
   a.kv_groups = (a.Hkv + U - 1) / U;
   a.groups = a.q_groups + 2 * a.kv_groups;
-  a.units = static_cast<int>(static_cast<int64_t>(a.T) * a.groups);
+  a.units = static_cast<uint32_t>(a.T) * static_cast<uint32_t>(a.groups);
   a.tokens_block = std::min(step, (step - 2 + a.groups) / a.groups + 1);
-  a.tiles = (a.units - 1) / step + 1;
-  const size_t smem = (V > 1 ? static_cast<size_t>(2 * U) * 2 * kRopeThreads * 16 : 0) +
+  a.tiles = static_cast<int>((a.units - 1) / step + 1);
+  const size_t smem = (V > 1 && U > 1 ? static_cast<size_t>(2 * U) * 2 * kRopeThreads * 16 : 0) +
                       2 * static_cast<size_t>(a.tokens_block) * (a.rot * sizeof(float) + 2 * sizeof(int64_t));
   static std::atomic<size_t> raised[2][kMaxDevices];
   const auto kern = U == 4 ? rope_kernel<TI, TC, V, 4, kCache> : rope_kernel<TI, TC, V, 1, kCache>;
@@ -352,7 +363,7 @@ cudaError_t launch_rows(RopeArgs& a, cudaStream_t stream) {
   if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return e;
   if (smem > 48 * 1024)
     if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem, raised[U == 4])) return e;
-  const dim3 grid(static_cast<unsigned>(std::min(a.tiles, sms * (U == 4 ? 3 : 8))));
+  const dim3 grid(static_cast<unsigned>(U == 4 && V > 1 ? std::min(a.tiles, sms * 3) : a.tiles));
   return launch_dependent<RopeArgs>(kern, grid, kRopeThreads, smem, stream, a);
 }
 
