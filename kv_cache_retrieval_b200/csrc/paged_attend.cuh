@@ -22,12 +22,14 @@
 // entry serves all of them.
 //
 // Products.  S^T = K Q^T (m16n8k16, tokens by heads: 8 heads fill n where a tile of 16 query rows would be half empty)
-// and O^T += V^T P^T, float32 sums.  P is a sum of two 16-bit values, exact to 2^-16 (bf16's 2^-8 alone would show in the
-// output); with an 8-bit cache and a bf16 output it is one fp16 value (2^-11, an eighth of the output's own rounding).
-// 8-bit elements become fp16 in registers, exactly; bf16 queries of an 8-bit cache become fp16 after a power of two per
-// row that makes their largest element about 2^14 (elements below 2^-28 of it lose bits).  mma.sync and not tcgen05: a
-// tile is 16 tokens of one warp, whose P never leaves its registers; the tensor pipe has room to spare, and a 128-row
-// tile with its commits would couple the warps that the private rings keep apart.
+// and O^T += V^T P^T, float32 sums.  P is a sum of 16-bit terms, by what the output's own rounding hides: three of bf16
+// for a float32 output (2^-25), two of bf16 for a bf16 output
+// (2^-17; one, 2^-8, would show), two of fp16 (2^-22), one of fp16 for a bf16 output of an 8-bit cache (2^-11, an eighth
+// of the output's rounding).  The tensor cores' sums lose up to a unit of their last place at every step, always towards
+// zero: for a float32 output a tile's product is a sum of its own, added by an ordinary addition.  8-bit elements become fp16 in registers, exactly; bf16 queries of an 8-bit cache become fp16
+// after a power of two per row that makes their largest element about 2^14 (elements below 2^-28 of it lose bits).
+// mma.sync and not tcgen05: a tile is 16 tokens of one warp, whose P never leaves its registers; the tensor pipe has room
+// to spare, and a 128-row tile with its commits would couple the warps that the private rings keep apart.
 #pragma once
 
 #include <algorithm>
@@ -194,21 +196,24 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two floats as a pair of 16-bit values (hi) and what they leave (lo).
-template <typename TM>
-__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
-  if constexpr (std::is_same<TM, __half>::value) {
-    const __half2 h = __floats2half2_rn(x, y);
-    const float2 f = __half22float2(h);
-    const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = *reinterpret_cast<const uint32_t*>(&l);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    const float2 f = __bfloat1622float2(h);
-    const __nv_bfloat162 l = __floats2bfloat162_rn(x - f.x, y - f.y);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = *reinterpret_cast<const uint32_t*>(&l);
+// Two floats as pairs of 16-bit values, one for each term: every one rounds what those before it leave.
+template <typename TM, int kTerms>
+__device__ __forceinline__ void split(float x, float y, uint32_t (&term)[kTerms]) {
+#pragma unroll
+  for (int k = 0; k < kTerms; ++k) {
+    if constexpr (std::is_same<TM, __half>::value) {
+      const __half2 h = __floats2half2_rn(x, y);
+      term[k] = *reinterpret_cast<const uint32_t*>(&h);
+      const float2 f = __half22float2(h);
+      x -= f.x;
+      y -= f.y;
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+      term[k] = *reinterpret_cast<const uint32_t*>(&h);
+      const float2 f = __bfloat1622float2(h);
+      x -= f.x;
+      y -= f.y;
+    }
   }
 }
 
@@ -321,13 +326,15 @@ __device__ __noinline__ void join_states(const PagedArgs& a, const Join* joins, 
   }
 }
 
-template <typename TQ, typename TC, int D, int NT, bool kPair>
+template <typename TQ, typename TC, int D, int NT, bool kFine>
 __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_kernel(const PagedArgs a) {
   using S = PagedShape<TQ, TC, D, NT>;
   using TM = typename S::TM;
   constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kDepth = S::kDepth, kRow = S::kRow, kTile = S::kTile;
   constexpr int kSub = S::kSub, kTokens = S::kTokens;
   constexpr uint32_t kAll = kSub == 2 ? ~0u : 0xffffu;
+  // terms of a weight (see the head of this file); kFine: the output is float32
+  constexpr int kTerms = std::is_same<TM, __nv_bfloat16>::value ? (kFine ? 3 : 2) : S::kE4 && !kFine && std::is_same<TQ, __nv_bfloat16>::value ? 1 : 2;
   constexpr int kLead = 2 * kDepth - 1;    // copy groups that may be in flight behind the one that is waited for
   // weights up to 2^14 in fp16: it keeps 2^-38 of the largest
   constexpr float kLift = std::is_same<TM, __half>::value ? 14.0f : 0.0f;
@@ -718,7 +725,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
               }
             }
         }
-        uint32_t hi[kSub][NT][2], lo[kSub][NT][2];
+        uint32_t p[kSub][NT][2][kTerms];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -734,9 +741,9 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
             l[n][1] += w[1] + w[3];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              split<TM>(w[2 * e], w[2 * e + 1], hi[i][n][e], lo[i][n][e]);
-              hi[i][n][e] = transposed(hi[i][n][e]);
-              if constexpr (kPair) lo[i][n][e] = transposed(lo[i][n][e]);
+              split<TM>(w[2 * e], w[2 * e + 1], p[i][n][e]);
+#pragma unroll
+              for (int k = 0; k < kTerms; ++k) p[i][n][e][k] = transposed(p[i][n][e][k]);
             }
           }
         copy_wait<kLead>();
@@ -749,8 +756,16 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
             const auto add = [&](int to, const uint32_t (&r)[4]) {
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                mma<TM>(o[n][to], r, hi[i][n][0], hi[i][n][1]);
-                if constexpr (kPair) mma<TM>(o[n][to], r, lo[i][n][0], lo[i][n][1]);
+                if constexpr (kFine) {
+                  float t[4] = {0, 0, 0, 0};
+#pragma unroll
+                  for (int k = kTerms - 1; k >= 0; --k) mma<TM>(t, r, p[i][n][0][k], p[i][n][1][k]);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[n][to][e] += t[e];
+                } else {
+#pragma unroll
+                  for (int k = 0; k < kTerms; ++k) mma<TM>(o[n][to], r, p[i][n][0][k], p[i][n][1][k]);
+                }
               }
             };
             uint32_t r[4];
@@ -937,11 +952,11 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
 }
 
 // Launches the variant for D and the heads of a unit.
-template <typename TQ, typename TC, int D, int NT, bool kPair>
+template <typename TQ, typename TC, int D, int NT, bool kFine>
 cudaError_t launch_paged_kernel(const PagedArgs& a, int grid, cudaStream_t s) {
   using S = PagedShape<TQ, TC, D, NT>;
   static std::atomic<size_t> raised[kMaxDevices];
-  const auto kern = paged_kernel<TQ, TC, D, NT, kPair>;
+  const auto kern = paged_kernel<TQ, TC, D, NT, kFine>;
   if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), S::kSmem, raised)) return e;
   return launch_dependent<PagedArgs>(kern, dim3(grid), S::kThreads, S::kSmem, s, a);
 }
@@ -950,28 +965,26 @@ cudaError_t launch_paged_kernel(const PagedArgs& a, int grid, cudaStream_t s) {
 inline int paged_max_heads(int d) { return d == 64 ? 32 : d == 128 ? 24 : 16; }
 
 template <typename TQ, typename TC, int D, int NT>
-cudaError_t launch_paged_pair(const PagedArgs& a, int grid, cudaStream_t s) {
-  if constexpr (std::is_same<TQ, __nv_bfloat16>::value && sizeof(TC) == 1)
-    if (!a.out_f32) return launch_paged_kernel<TQ, TC, D, NT, false>(a, grid, s);
-  return launch_paged_kernel<TQ, TC, D, NT, true>(a, grid, s);
+cudaError_t launch_paged_out(const PagedArgs& a, int grid, cudaStream_t s) {
+  return a.out_f32 ? launch_paged_kernel<TQ, TC, D, NT, true>(a, grid, s) : launch_paged_kernel<TQ, TC, D, NT, false>(a, grid, s);
 }
 
 template <typename TQ, typename TC>
 cudaError_t launch_paged_typed(const PagedArgs& a, int d, int grid, cudaStream_t s) {
   const int nt = (a.chunk + 7) / 8;
   if (d == 64) {
-    if (nt == 1) return launch_paged_pair<TQ, TC, 64, 1>(a, grid, s);
-    if (nt == 2) return launch_paged_pair<TQ, TC, 64, 2>(a, grid, s);
-    if (nt == 3) return launch_paged_pair<TQ, TC, 64, 3>(a, grid, s);
-    return launch_paged_pair<TQ, TC, 64, 4>(a, grid, s);
+    if (nt == 1) return launch_paged_out<TQ, TC, 64, 1>(a, grid, s);
+    if (nt == 2) return launch_paged_out<TQ, TC, 64, 2>(a, grid, s);
+    if (nt == 3) return launch_paged_out<TQ, TC, 64, 3>(a, grid, s);
+    return launch_paged_out<TQ, TC, 64, 4>(a, grid, s);
   }
   if (d == 128) {
-    if (nt == 1) return launch_paged_pair<TQ, TC, 128, 1>(a, grid, s);
-    if (nt == 2) return launch_paged_pair<TQ, TC, 128, 2>(a, grid, s);
-    return launch_paged_pair<TQ, TC, 128, 3>(a, grid, s);
+    if (nt == 1) return launch_paged_out<TQ, TC, 128, 1>(a, grid, s);
+    if (nt == 2) return launch_paged_out<TQ, TC, 128, 2>(a, grid, s);
+    return launch_paged_out<TQ, TC, 128, 3>(a, grid, s);
   }
-  if (nt == 1) return launch_paged_pair<TQ, TC, 256, 1>(a, grid, s);
-  return launch_paged_pair<TQ, TC, 256, 2>(a, grid, s);
+  if (nt == 1) return launch_paged_out<TQ, TC, 256, 1>(a, grid, s);
+  return launch_paged_out<TQ, TC, 256, 2>(a, grid, s);
 }
 
 // One translation unit per pair of types (paged_*.cu).
