@@ -409,8 +409,8 @@ int32_t hhr_rope(int32_t T, int32_t H, int32_t d, int32_t type, const hhr_rotati
  * at offset n % page of page table[b * table_stride + n / page].
  * With HHR_TYPE_E4M3 a stored element stands for k_scale (v_scale) times its value.
  * Supported: d in {64, 128, 256}; Hq % Hkv == 0; q_type BF16 or F16; kv_type
- * q_type or E4M3; page >= 1; table_cols * page < 2^31; strides > 0 and a
- * multiple of 16 bytes.
+ * q_type or E4M3; page >= 1; table_cols * page < 2^31; Hq * d < 2^31; strides
+ * > 0 and a multiple of 16 bytes.
  */
 typedef struct hhr_paged {
   int32_t Hq;           /* query heads                                     */
@@ -460,8 +460,8 @@ int32_t hhr_paged_append(const hhr_paged* cache, int32_t T, int32_t B,
                          void* V, uint32_t* status, void* stream);
 
 /*
- * Bytes of device workspace hhr_paged_attend needs for this cache on the
- * current device; 0 if the cache is invalid.  Zero-filled once before its
+ * Bytes of device workspace hhr_paged_attend needs for this cache; 0 if the
+ * cache is invalid.  Zero-filled once before its
  * first use, left in that state by every call; not to be shared by two calls
  * that may run at the same time (two captured graphs included).  It does not
  * depend on the number of sequences or their lengths.
@@ -483,6 +483,9 @@ size_t hhr_paged_workspace_size(const hhr_paged* cache);
  *   lse      device, write, nullable: f32 [B][Hq].
  *   workspace device: at least hhr_paged_workspace_size(cache) bytes.
  * Lengths and pages are read on the device, so a captured call follows them.
+ * Supported: B * Hq < 2^31, B * Hq * table_cols * page < 2^40.  scale: any
+ * finite value.  A logit of -inf leaves its token out; other non-finite values
+ * among a sequence's tokens make its outputs non-finite.
  * A length outside [0, table_cols * page] counts as 0 and a page outside
  * [0, n_pages) as masked tokens; either sets the workspace status word to
  * HHR_ERR_BAD_INDEX (hhr_read_status) and leaves the workspace usable.
