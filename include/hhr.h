@@ -409,7 +409,7 @@ int32_t hhr_rope(int32_t T, int32_t H, int32_t d, int32_t type, const hhr_rotati
  * at offset n % page of page table[b * table_stride + n / page].
  * With HHR_TYPE_E4M3 a stored element stands for k_scale (v_scale) times its value.
  * Supported: d in {64, 128, 256}; Hq % Hkv == 0; q_type BF16 or F16; kv_type
- * q_type or E4M3; page >= 1; table_cols * page < 2^31; Hq * d < 2^31; strides
+ * q_type or E4M3; page >= 1; table_cols * page <= 2^31 - 64; Hq * d < 2^31; strides
  * > 0 and a multiple of 16 bytes.
  */
 typedef struct hhr_paged {

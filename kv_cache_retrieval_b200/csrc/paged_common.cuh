@@ -48,7 +48,8 @@ inline int32_t check_paged(const hhr_paged* c) {
     if (s < 1 || s % unit != 0) return HHR_ERR_INVALID_ARG;
   if (c->d != 64 && c->d != 128 && c->d != 256) return HHR_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(c->Hq) * c->d >= (int64_t{1} << 31)) return HHR_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(c->table_cols) * c->page >= (int64_t{1} << 31)) return HHR_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(c->table_cols) * c->page > (int64_t{1} << 31) - 64) return   // a tile's rows behind the last one have numbers too
+    HHR_ERR_UNSUPPORTED;
   return HHR_OK;
 }
 

@@ -72,12 +72,13 @@ class HHRPagedCache:
 
     def _table(self, table):
         """A reference to the description with this table's columns and row stride, and the table's rows."""
-        if table.dim() != 2 or table.dtype is not torch.int32 or table.get_device() != self._index or \
-                (table.shape[1] > 1 and table.stride(1) != 1):
+        shape, strides = table.shape, table.stride()
+        if len(shape) != 2 or table.dtype is not torch.int32 or table.get_device() != self._index or \
+                (shape[1] > 1 and strides[1] != 1):
             raise ValueError(f"table: expected int32 [sequences, pages] on {self.device} with adjacent columns, "
                              f"got {table.dtype} {tuple(table.shape)} on {table.device}")
-        rows, cols = table.shape
-        stride = table.stride(0) if rows > 1 else cols
+        rows, cols = shape
+        stride = strides[0] if rows > 1 else cols
         desc = self._descs.get((cols, stride))
         if desc is None:   # never changed after this: another thread's call may be reading it
             desc = B.hhr_paged.from_buffer_copy(self.desc)
@@ -88,15 +89,15 @@ class HHRPagedCache:
         return desc, rows
 
     def _rows(self, name, t, heads):
-        """Elements between two tokens' rows of t [T, heads, head_dim]."""
-        d = self._d
-        if t.dim() != 3 or t.dtype is not self.dtype or t.get_device() != self._index or t.shape[1] != heads or t.shape[2] != d:
+        """T of t [T, heads, head_dim] and the elements between two of its rows."""
+        d, shape = self._d, t.shape
+        if len(shape) != 3 or t.dtype is not self.dtype or t.get_device() != self._index or shape[1] != heads or shape[2] != d:
             raise ValueError(f"{name}: expected {self.dtype} [tokens, {heads}, {d}] on {self.device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
         row, head, one = t.stride()
         if one != 1 or (heads > 1 and head != d):
             raise ValueError(f"{name}: a token's heads have to be adjacent")
-        return row
+        return shape[0], row
 
     def append(self, k, v, positions, table, *, seq=None, q=None, q_out=None, freqs=None, rope_positions=None,
                interleaved=False, mscale=1.0):
@@ -105,13 +106,14 @@ class HHRPagedCache:
         (rows of `table`; None: token t of sequence t).  freqs (rope_freqs): the keys
         are rotated by rope_positions (None: positions) on the way, and with q
         [T, q_heads, head_dim] the queries too, into q_out (a new tensor if
-        None; q itself rotates in place).  Returns q_out."""
+        None; q itself rotates in place).  Returns q_out.  Writes the pools in place: no
+        gradient passes through it."""
         index = self._index
         desc, rows = self._table(table)
-        T = k.shape[0]
-        k_row, v_row = self._rows("k", k, self._Hkv), self._rows("v", v, self._Hkv)
-        if v.shape[0] != T:
-            raise ValueError(f"v: {v.shape[0]} tokens, k has {T}")
+        T, k_row = self._rows("k", k, self._Hkv)
+        v_T, v_row = self._rows("v", v, self._Hkv)
+        if v_T != T:
+            raise ValueError(f"v: {v_T} tokens, k has {T}")
         check_vector("positions", positions, torch.int32, T, index)
         if seq is not None:
             check_vector("seq", seq, torch.int32, T, index)
@@ -121,15 +123,17 @@ class HHRPagedCache:
         if q is not None:
             if q_out is None:
                 q_out = q.new_empty(q.shape)
-            q_tok, o_tok = self._rows("q", q, self._Hq), self._rows("q_out", q_out, self._Hq)
-            if q.shape[0] != T or q_out.shape[0] != T:
-                raise ValueError(f"q, q_out: {q.shape[0]} and {q_out.shape[0]} tokens, k has {T}")
+            q_T, q_tok = self._rows("q", q, self._Hq)
+            o_T, o_tok = self._rows("q_out", q_out, self._Hq)
+            if q_T != T or o_T != T:
+                raise ValueError(f"q, q_out: {q_T} and {o_T} tokens, k has {T}")
         elif q_out is not None:
             raise ValueError("q_out without q")
         rot = None
         if freqs is not None:
-            check_vector("freqs", freqs, torch.float64, freqs.numel(), index)
-            rot = rotation(2 * freqs.shape[0], B.HHR_ROPE_INTERLEAVED if interleaved else 0, mscale)
+            half = freqs.numel()
+            check_vector("freqs", freqs, torch.float64, half, index)
+            rot = rotation(2 * half, B.HHR_ROPE_INTERLEAVED if interleaved else 0, mscale)
         st = on_device(index, B.lib().hhr_paged_append, desc, T, rows, rot, None if freqs is None else freqs.data_ptr(),
                        positions.data_ptr(), None if rope_positions is None else rope_positions.data_ptr(),
                        None if seq is None else seq.data_ptr(), table.data_ptr(), None if q is None else q.data_ptr(), q_tok,
@@ -144,20 +148,20 @@ class HHRPagedCache:
         each sequence, or the last `window` of them; into out (dtype or float32;
         a new tensor of dtype if None) and lse (float32 [B, q_heads], optional).
         scale: 1/sqrt(head_dim) if None.  workspace (new_workspace): needed by calls that may
-        run at the same time as another one on this cache."""
+        run at the same time as another one on this cache.  A serving call: it has no gradient."""
         index = self._index
         desc, rows = self._table(table)
-        q_seq = self._rows("q", q, self._Hq)
-        if q.shape[0] != rows:
-            raise ValueError(f"q: {q.shape[0]} sequences, table has {rows}")
+        q_B, q_seq = self._rows("q", q, self._Hq)
+        if q_B != rows:
+            raise ValueError(f"q: {q_B} sequences, table has {rows}")
         check_vector("lens", lens, torch.int32, rows, index)
         if out is None:
             out = q.new_empty(q.shape)
         elif out.shape != q.shape or (out.dtype is not self.dtype and out.dtype is not torch.float32) or \
                 out.get_device() != index or not out.is_contiguous():
             raise ValueError(f"out: expected a contiguous {self.dtype} or float32 tensor {tuple(q.shape)} on {self.device}")
-        if lse is not None and (lse.dtype is not torch.float32 or lse.dim() != 2 or lse.shape[0] != rows or
-                                lse.shape[1] != self._Hq or lse.get_device() != index or not lse.is_contiguous()):
+        if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (rows, self._Hq) or
+                                lse.get_device() != index or not lse.is_contiguous()):
             raise ValueError(f"lse: expected a contiguous float32 tensor [{rows}, {self._Hq}] on {self.device}")
         if workspace is None:
             workspace = self.workspace

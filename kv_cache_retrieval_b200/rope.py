@@ -37,7 +37,7 @@ def on_device(index, fn, *args):
 
 def check_vector(name, t, dtype, length, index):
     """t: contiguous [length] of dtype on CUDA device `index`."""
-    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != length or t.get_device() != index or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != (length,) or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} [{length}] on cuda:{index}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
@@ -90,10 +90,11 @@ def rope(x, positions, freqs, *, interleaved=False, mscale=1.0, out=None):
     """x [T, H, d] (bf16, fp16 or fp32; any token and head strides) with its first 2 * freqs.numel() elements
     rotated by positions[t] * freqs (hhr_rope).  positions: int32 [T]; freqs: float64 [rot/2].  Differentiable
     with respect to x.  out: where to put the result (x itself rotates in place); not with a gradient."""
-    if x.dim() != 3 or x.dtype not in _TYPES or not x.is_cuda:
+    shape = x.shape
+    if len(shape) != 3 or x.dtype not in _TYPES or not x.is_cuda:
         raise ValueError(f"x: expected a bf16, fp16 or fp32 CUDA tensor [T, H, d], got {x.dtype} {tuple(x.shape)} on {x.device}")
     index = x.get_device()
-    check_vector("positions", positions, torch.int32, x.shape[0], index)
+    check_vector("positions", positions, torch.int32, shape[0], index)
     check_vector("freqs", freqs, torch.float64, freqs.numel(), index)
     flags = B.HHR_ROPE_INTERLEAVED if interleaved else 0
     if x.requires_grad and torch.is_grad_enabled():
@@ -101,9 +102,9 @@ def rope(x, positions, freqs, *, interleaved=False, mscale=1.0, out=None):
             raise ValueError("out= has no gradient: call without it, or on x.detach()")
         return _Rope.apply(x, positions, freqs, flags, mscale)
     if out is None:
-        out = x.new_empty(x.shape)
-    elif out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != index or \
-            (out.stride(2) != 1 and x.shape[2] > 1):
+        out = x.new_empty(shape)
+    elif out.shape != shape or out.dtype is not x.dtype or out.get_device() != index or \
+            (out.stride(2) != 1 and shape[2] > 1):
         raise ValueError(f"out: expected {x.dtype} {tuple(x.shape)} on {x.device} with adjacent elements of a head, "
                          f"got {out.dtype} {tuple(out.shape)} on {out.device}")
     return _rotate(x, positions, freqs, flags, mscale, out)

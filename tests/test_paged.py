@@ -763,6 +763,35 @@ def test_two_streams_with_their_own_workspaces():
 
 
 @pytest.mark.gpu
+def test_two_threads_with_tables_of_their_own():
+    """Two Python threads on one cache, with tables of different widths: each call has its own description."""
+    import threading
+    c, q, t = make(2, 8, 2, 64, 16, 60)
+    tables, lens = (t[:, :20].contiguous(), t), ([320, 37], [960, 500])
+    want, got, bad = [], [[], []], []
+    for tab, n in zip(tables, lens):
+        want.append(c.attend(q, tab, torch.tensor(n, dtype=torch.int32, device="cuda")).clone())
+    spaces = [c.new_workspace() for _ in range(2)]
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()) as _:
+                n = torch.tensor(lens[i], dtype=torch.int32, device="cuda")
+                for _ in range(200):
+                    got[i].append(c.attend(q, tables[i], n, workspace=spaces[i]))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001 - reported by the main thread
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [x.start() for x in threads]
+    [x.join() for x in threads]
+    assert not bad, bad
+    assert all(torch.equal(o, want[i]) for i in range(2) for o in got[i])
+
+
+@pytest.mark.gpu
 def test_hhr_cache_append_and_dense_attention():
     """The retrieval cache takes unrotated tokens: rotated and stored, encoded as hhr_encode_keys does, and its keys and
     values serve attention with a length for each sequence."""
