@@ -5,7 +5,8 @@ Tolerances.  An appended element is the rotated one's float32 value (12 half ste
 test_rope.py) rounded once to the cache's type.  For attention let w_n be the softmax weights: the logits' float32
 error is at most (d + 4) 2^-24 scale sum_e |q_e k_e| =: e_n for a d-term sum in any order and its scaling, which moves
 each weight by a factor exp(+-2 max_n e_n); weights, sums and merges round to float32 (or a pair of 16-bit values that
-holds 2^-16; with a bf16 output of an 8-bit cache one fp16 value, 2^-11), so with c = 2^-15 (or 2^-11 + 2^-15) + 2 max e_n the output is within (c + 2^-24 rounds) sum_n w_n |v_n| + its own rounding.
+holds 2^-16; with a bf16 output of an 8-bit cache one fp16 value, 2^-11), so with c = 2^-15 (or 2^-11 + 2^-15) + 2 max e_n
+the output is within (c + 2^-24 rounds) sum_n w_n |v_n| + its own rounding.
 The growth of float32 sums over n tokens is covered by 2^-24 (tokens of one lane + merges) <= 2^-24 (n / 16 + 64).  The
 log-sum-exp is within max e_n + 2^-24 (n / 16 + 64) + 2^-22 |lse|."""
 import ctypes as C
