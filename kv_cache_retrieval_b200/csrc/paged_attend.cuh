@@ -416,12 +416,18 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
   if (tid < 2 * kWarps) s_open[tid].x1 = 0;
   __syncthreads();
   total *= units;
-  // G CTAs take part.  Where that is not all of them it is a multiple of the units, so that equal ones are not shared.
-  int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(int64_t{1}, total / (kWarps * a.min_tiles))));
-  if (G < gridDim.x && static_cast<int64_t>(n_seqs) * units <= G) G -= G % (n_seqs * units);
+  // G CTAs take part with n_active warps each.  Where the tiles do not fill the card, G is a multiple of the units, so
+  // that units of one length are not shared by CTAs (calls: 43 sequences of 3 tokens, 2 KV heads 9 us, with the tiles
+  // packed into few CTAs 16; 9 sequences, window 128, 2 KV heads, groups of 24 25 us, with units shared 30).
+  const int64_t n_units = static_cast<int64_t>(n_seqs) * units;
+  const int64_t fill = total / (kWarps * a.min_tiles);
+  const int G = static_cast<int>(fill >= gridDim.x || n_units > gridDim.x
+                                     ? min(static_cast<int64_t>(gridDim.x), max(int64_t{1}, total))
+                                     : max(int64_t{1}, max(int64_t{1}, fill / max(int64_t{1}, n_units)) * n_units));
+  const int n_active = static_cast<int>(min(static_cast<int64_t>(kWarps), max(int64_t{1}, total / G)));
   const int c = blockIdx.x;
   // Warp i of them takes [first_of(i), first_of(i + 1)), a tile at least (the host bounds total * n_warps).
-  const uint32_t n_warps = static_cast<uint32_t>(max(int64_t{1}, min(static_cast<int64_t>(G) * kWarps, total)));
+  const uint32_t n_warps = G * n_active;
   const int64_t quot = total >> 32 ? total / n_warps : static_cast<int64_t>(static_cast<uint32_t>(total) / n_warps);
   const uint32_t rem = static_cast<uint32_t>(total - quot * n_warps);
   const auto first_of = [&](uint32_t i) {
@@ -429,10 +435,10 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
     return quot * i + rem * i / n_warps;
   };
   const auto cta_of = [&](int64_t x) {   // of the warp whose range holds x: the last with total * i / n_warps <= x
-    return static_cast<int>((static_cast<uint64_t>(x + 1) * n_warps - 1) / static_cast<uint64_t>(total)) / kWarps;
+    return static_cast<int>((static_cast<uint64_t>(x + 1) * n_warps - 1) / static_cast<uint64_t>(total)) / n_active;
   };
-  const int64_t f0 = first_of(c * kWarps), f1 = first_of((c + 1) * kWarps);
-  const int64_t w0 = first_of(c * kWarps + warp), w1 = first_of(c * kWarps + warp + 1);
+  const int64_t f0 = first_of(c * n_active), f1 = first_of((c + 1) * n_active);
+  const int64_t w0 = first_of(c * n_active + warp), w1 = warp < n_active ? first_of(c * n_active + warp + 1) : w0;
 
   if (w0 < w1) {
     // ---- where w0 lies: the last run that begins at or before it, then the sequence
