@@ -23,8 +23,10 @@
 //
 // Products.  S^T = K Q^T (m16n8k16, tokens by heads: 8 heads fill n where a tile of 16 query rows would be half empty)
 // and O^T += V^T P^T, float32 sums.  P is a sum of 16-bit terms, by what the output's own rounding hides: three of bf16
-// for a float32 output (2^-25), two of bf16 for a bf16 output (2^-17; one, 2^-8, would show), two of fp16 (2^-22), one
-// of fp16 for a bf16 output of an 8-bit cache (2^-11, an eighth of the output's rounding).  The tensor cores' own sums
+// for a float32 output (2^-25), two of bf16 for a bf16 output (2^-17; one, 2^-8, would show; three change 0.3 % of the
+// values by a step and cost 8 % in groups of 12 to 24 heads), two of fp16 (2^-22; one, 2^-11, is an eighth of a bf16
+// output's rounding, but moves 6 % of its values a step from the float32 result's rounding where two move 0.1 %; it
+// takes 53 us where two take 59, 16 heads, 8-bit cache).  The tensor cores' own sums
 // lose up to a unit of their last place at every step: for a float32 output a tile's product is a sum of its own, added
 // by an ordinary addition (128K tokens: relative error 1.9e-6 without, 5e-7 with it).  8-bit elements become fp16 in
 // registers, exactly; bf16 queries of an 8-bit cache become fp16 after a power of two per row that makes their largest
@@ -34,7 +36,7 @@
 //
 // Measured (B200, captured passes): 1 x 128K, 8 KV heads of 128, bf16: 86 us, 6.25 TB/s (0.97 of the copy bandwidth);
 // 8 x 64K: 305 us, 7.0 TB/s; 61 ragged sequences to 8191, groups of 8, fp16: 116 us, 5.6 TB/s; 16 ragged to 32K, 4 KV
-// heads, groups of 16, e4m3: 53 us, 2.8 TB/s (issue and latency of the conversions and products, then the joins); one
+// heads, groups of 16, e4m3: 59 us, 2.5 TB/s (issue and latency of the conversions and products, then the joins); one
 // sequence of 517: 9.6 us (latency).  DRAM reads are 1.00 of the keys and values.
 #pragma once
 
@@ -87,7 +89,7 @@ struct PagedShape {
   static constexpr int kTile = kTokens * kRow;
   static constexpr int kHeads = 8 * NT;
   // Registers hold the query fragments of 8 heads; those of more are read from shared memory, each warp its own copy
-  // (16 heads, d = 128, 8-bit: 58 us in registers of 8 warps, 55 of 12 warps with spills, 53 from shared memory).
+  // (16 heads, d = 128, 8-bit, one term a weight: 58 us in registers of 8 warps, 55 of 12 warps, 53 from shared memory).
   static constexpr bool kQRegs = NT == 1;
   // More warps hide more latency where their registers allow it.  The rings together hold about 100 KB: with 192 KB in
   // flight the SMs at the head of their group run 25 % ahead of the last ones and the call waits for those (8 sequences
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
   constexpr int kSub = S::kSub, kTokens = S::kTokens;
   constexpr uint32_t kAll = kSub == 2 ? ~0u : 0xffffu;
   // terms of a weight (see the head of this file); kFine: the output is float32
-  constexpr int kTerms = std::is_same<TM, __nv_bfloat16>::value ? (kFine ? 3 : 2) : S::kE4 && !kFine && std::is_same<TQ, __nv_bfloat16>::value ? 1 : 2;
+  constexpr int kTerms = std::is_same<TM, __nv_bfloat16>::value && kFine ? 3 : 2;
   constexpr int kLead = 2 * kDepth - 1;    // copy groups that may be in flight behind the one that is waited for
   // weights up to 2^14 in fp16: it keeps 2^-38 of the largest
   constexpr float kLift = std::is_same<TM, __half>::value ? 14.0f : 0.0f;
