@@ -1,9 +1,10 @@
 // The kernel of hhr_paged_attend: attention of one new token per sequence over
 // a paged key-value cache, split over the cache's length and joined.
 //
-// out[h] = sum_n w_n V[n] / sum_n w_n with w_n = 2^(x_n - m), x_n = scale log2(e) q[h].K[n], m the largest x_n: one pass
-// over K and V with a running m, rescaling what was summed whenever m grows; states of disjoint token ranges (m, sum w,
-// sum w V) join by rescaling to the larger m.
+// out[h] = sum_n w_n V[n] / sum_n w_n with w_n = 2^((x_n - m) c), x_n = q[h].K[n], c = scale log2(e), m the largest x_n:
+// one pass over K and V with a running m, rescaling what was summed whenever m grows; states of disjoint token ranges
+// (m, sum w, sum w V) join by rescaling to the larger m.  The difference is taken before the scale: it rounds at its own
+// size and not at the logits', and a mask by a type's lowest value cannot overflow on the way.
 //
 // Bound: HBM.  A token costs 2 d elements of K and V per KV head and 4 d r operations for its r query heads: 2 to 24
 // operations per byte, far below what the tensor cores do in that time, so the work is to keep loads in flight.
@@ -250,13 +251,22 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t turned, int c) {   // turn
   return (turned ^ ((c & 7) << 4)) + (c >> 3) * 128;
 }
 
-// The weight of a state of maximum m among states of maximum top; 1 / sum of a unit's weights (0 for none, NaN stays)
-// and its log-sum-exp.
-__device__ __forceinline__ float paged_weight(float m, float top) { return m == top ? 1.0f : ex2(m - top); }
+// The maximum of a state is exchanged as a quarter of its logit in powers of two: a finite logit times log2(e) may be
+// beyond float32.  The weight of a state of maximum m among states of maximum top; 1 / sum of a unit's weights (0 for
+// none, NaN stays) and its log-sum-exp, where the weights are 2^lift times what they stand for.
+__device__ __forceinline__ float paged_quarter(float m, float scale) { return m == -INFINITY ? m : m * (scale * 0.25f); }
+__device__ __forceinline__ float paged_weight(float m, float top) { return m == top ? 1.0f : ex2((m - top) * 4.0f); }
 __device__ __forceinline__ float paged_inverse(float sum, float scale) { return sum > 0 ? scale / sum : sum; }
-__device__ __forceinline__ float paged_log_sum(float top, float sum) {
-  return sum == 0 ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+__device__ __forceinline__ float paged_log_sum(float top, float sum, float lift) {
+  constexpr float kLn2 = 0.69314718055994530942f;
+  return sum == 0 ? -INFINITY : fmaf(top, 4.0f * kLn2, (log2f(sum) - lift) * kLn2);
 }
+
+// Weights of fp16 terms are lifted to 2^14 at most: fp16 keeps 2^-38 of the largest.  The lift is added to a difference
+// from the largest (it rounds to 2^-21 there): subtracted from the largest logit it would round at the logit's size, to
+// 16 and a weight beyond fp16 where logits reach 2^25.
+template <typename TM>
+__device__ constexpr float kPagedLift = std::is_same<TM, __half>::value ? 14.0f : 0.0f;
 
 // A join of n states: the i-th at base + i * stride, the last at `last` unless that is null; into the state `to` (none of
 // these), or, if that is null, into the output's rows from out_row on.
@@ -271,7 +281,7 @@ struct Join {
 
 // All threads of a CTA do `count` joins side by side, a thread four columns of a head at a time.  One copy of this code
 // serves all joins: it is fetched cold.
-template <typename TQ, int D, int kThreads>
+template <typename TQ, typename TM, int D, int kThreads>
 __device__ __noinline__ void join_states(const PagedArgs& a, const Join* joins, int count) {
   const int most = a.chunk * (D / 4);
 #pragma unroll 1
@@ -334,7 +344,7 @@ __device__ __noinline__ void join_states(const PagedArgs& a, const Join* joins, 
       p.v[3] = from_f32<TQ>(y.w * inv);
       *reinterpret_cast<Pack<TQ, 4>*>(static_cast<TQ*>(a.out) + at) = p;
     }
-    if (d == 0 && a.lse) a.lse[j.out_row + h] = paged_log_sum(top, sum);
+    if (d == 0 && a.lse) a.lse[j.out_row + h] = paged_log_sum(top, sum, kPagedLift<TM>);
   }
 }
 
@@ -348,8 +358,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
   // terms of a weight (see the head of this file); kFine: the output is float32
   constexpr int kTerms = std::is_same<TM, __nv_bfloat16>::value && kFine ? 3 : 2;
   constexpr int kLead = 2 * kDepth - 1;    // copy groups that may be in flight behind the one that is waited for
-  // weights up to 2^14 in fp16: it keeps 2^-38 of the largest
-  constexpr float kLift = std::is_same<TM, __half>::value ? 14.0f : 0.0f;
+  constexpr float kLift = kPagedLift<TM>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t s_scan[kWarps], s_before[kThreads];
   __shared__ Join s_join[kWarps + 1];
@@ -634,7 +643,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
         for (int e = 0; e < 2; ++e) {
           sc[n][e] = __shfl_sync(~0u, up, (2 * t4 + e) * 4);
           m[n][e] = -INFINITY;        // the largest product so far
-          base[n][e] = l[n][e] = 0;   // weights are 2^(product * sc - base) with base = m * sc - kLift
+          base[n][e] = l[n][e] = 0;   // m, or 0 while there is none: products of -inf weigh nothing
         }
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
@@ -730,11 +739,8 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
               top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
               top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
               if (top > m[n][e]) {   // the same for the 8 lanes of a column
-                // rounded as the logits below are: at the size of a mask by the lowest value the rounding is no small thing
-                const float next = __fmul_rn(top, sc[n][e]) - kLift;
-                const float by = m[n][e] == -INFINITY ? 1.0f : ex2(base[n][e] - next);
-                m[n][e] = top;
-                base[n][e] = next;
+                const float by = m[n][e] == -INFINITY ? 1.0f : ex2((m[n][e] - top) * sc[n][e]);
+                m[n][e] = base[n][e] = top;
                 l[n][e] *= by;
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
@@ -751,7 +757,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
           for (int i = 0; i < kSub; ++i) {
             float w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = ex2(__fmul_rn(s[i][0][n][e], sc[n][e & 1]) - base[n][e & 1]);
+            for (int e = 0; e < 4; ++e) w[e] = ex2(fmaf(s[i][0][n][e] - base[n][e & 1], sc[n][e & 1], kLift));
             if (some) {   // (a scale of zero makes them numbers)
               if (!((rows >> (16 * i + g)) & 1)) w[0] = w[1] = 0;
               if (!((rows >> (16 * i + g + 8)) & 1)) w[2] = w[3] = 0;
@@ -826,7 +832,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
             if (h >= heads) continue;
             const float inv = paged_inverse(l[n][e], a.v_scale);
             const size_t row = static_cast<size_t>(seg.b) * a.Hq + head0 + h;
-            if (a.lse && g == 0) a.lse[row] = paged_log_sum(base[n][e], l[n][e]);
+            if (a.lse && g == 0) a.lse[row] = paged_log_sum(paged_quarter(m[n][e], sc[n][e]), l[n][e], kLift);
 #pragma unroll
             for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -859,7 +865,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
                 row[j * 16 + g + 8] = o[n][j][e + 2];
               }
             }
-            if (g == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[n][e] == -INFINITY ? -INFINITY : base[n][e], l[n][e]);
+            if (g == 0) *reinterpret_cast<float2*>(row + D) = make_float2(paged_quarter(m[n][e], sc[n][e]), l[n][e]);
           }
         if (lane == 0) s_open[2 * warp + last] = {x0, x1, seg.b, seg.u};
       }
@@ -912,7 +918,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
     }
   }
   __syncthreads();
-  join_states<TQ, D, kThreads>(a, s_join, s_joins);
+  join_states<TQ, TM, D, kThreads>(a, s_join, s_joins);
 
   if (s_side[0] >= 0 || s_side[1] >= 0) {
     // Units shared with CTAs before (0) and behind (1).  The last of a unit's CTAs to arrive joins their states from L2.
@@ -946,7 +952,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
     __syncthreads();
 #pragma unroll 1
     for (int side = 0; side < 2; ++side)
-      if (s_last[side]) join_states<TQ, D, kThreads>(a, s_join + s_side[side], 1);
+      if (s_last[side]) join_states<TQ, TM, D, kThreads>(a, s_join + s_side[side], 1);
   }
 
   // Rows of sequences without tokens, and lengths out of range.

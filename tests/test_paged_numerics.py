@@ -44,3 +44,68 @@ def test_weights_of_an_8_bit_cache_are_not_rounded_to_16_bits(dtype, r):
     out, _, lens = attend(c, q, t, [640, 9, 100, 333], dtype)
     o, _, tol, _, _ = attend64(c, q, t, lens, scales=scales)
     close(out, o, tol)
+
+
+TYPES = [(BF, BF), (FP16, FP16), (BF, E4), (FP16, E4)]
+
+
+@pytest.mark.parametrize("dtype,kv", TYPES)
+@pytest.mark.parametrize("n", [1, 3, 40, 2000])
+def test_equal_logits_of_any_size_average_the_values(dtype, kv, n):
+    """Keys that all give one logit x, up to what float32 holds: weights of 1 / n, and ln n + x.  The logits are powers
+    of two, exact in every step, so the output has the errors of its float32 sums alone (n / 16 + 64 additions)."""
+    c, q, t = make(1, 4, 2, 64, 16, 125, dtype=dtype, kv=kv)
+    q.zero_()
+    q[..., 5] = 16.0
+    c.K.zero_()
+    v = c.V.float()[t[0].long()].transpose(1, 2).reshape(2000, 2, 64)[:n].double().cpu()
+    tol = 2.0 ** -24 * (n / 16 + 64) * v.abs().mean(0).repeat_interleave(2, 0)[None]
+    for power in [0, 20, 23, 24, 25, 26, 27, 28, 30, 60, 100, 127]:
+        for sign in (1.0, -1.0):
+            c.K[..., 5] = torch.tensor(sign * 16.0).to(kv)
+            x = sign * 2.0 ** power
+            for out_dtype in (F32, dtype):
+                out, lse, _ = attend(c, q, t, [n], out_dtype, scale=2.0 ** (power - 8))
+                close(out, v.mean(0).repeat_interleave(2, 0)[None], tol)
+                err = (lse.double().cpu() - (x + math.log(n))).abs().max()
+                assert float(err) <= 2.0 ** -22 * abs(x + math.log(n)) + 2.0 ** -20, (power, sign)
+
+
+@pytest.mark.parametrize("dtype,kv", TYPES)
+@pytest.mark.parametrize("power", [23, 24, 25, 26])
+def test_far_lower_logits_before_ordinary_ones(dtype, kv, power):
+    """Whole tiles whose logits are -2^power, as a mask in the keys gives them, before and between ordinary tokens."""
+    scales = (2.0 ** 6, 1.0) if kv == E4 else (1.0, 1.0)
+    c, q, t = make(1, 4, 1, 128, 16, 60, dtype=dtype, kv=kv, scales=scales, hot=False)
+    at = torch.arange(960)
+    low = (at < 100) | ((at >= 300) & (at < 500)) | (at % 7 == 3) | (at > 900)
+    n = torch.nonzero(low)[:, 0]
+    q[..., 0] = 2.0 ** (power + 3 - 14)
+    c.K[..., 0] = 0
+    c.K[t[0].cpu()[n // 16].long().cuda(), 0, (n % 16).cuda(), 0] = torch.tensor(-2.0 ** 14 / scales[0]).to(kv)
+    for out_dtype in (F32, dtype):
+        out, lse, lens = attend(c, q, t, [960], out_dtype, scale=0.125)
+        o, l, tol, ltol, _ = attend64(c, q, t, lens, scale=0.125, scales=scales, live=[~low])
+        close(out, o, tol)
+        assert bool(((lse.double().cpu() - l).abs() <= ltol).all())
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.5, 2.0])
+def test_lowest_values_at_any_scale(scale):
+    """A mask by the lowest bf16 value whose logit in powers of two (times log2 e) is beyond float32: alone it averages,
+    before ordinary tokens it leaves no trace."""
+    c, q, t = make(1, 4, 1, 64, 16, 8, hot=False)
+    q[..., 0] = 1.0
+    c.K[..., 0] = torch.finfo(BF).min
+    out, _, _ = attend(c, q, t, [100], F32, scale=scale)
+    v = c.V.float()[t[0].long()].transpose(1, 2).reshape(128, 64)[:100].double().cpu()
+    if scale <= 1.0:      # (twice the lowest value is a logit of -inf)
+        # the other products are below half a step of the mask's
+        close(out, v.mean(0).expand(1, 4, 64), 2.0 ** -24 * 128 * v.abs().mean(0).expand(1, 4, 64))
+    c.K[int(t[0, 5]), 0, 3:9, 0] = 0.0
+    live = torch.zeros(128, dtype=torch.bool)
+    live[83:89] = True
+    out, lse, lens = attend(c, q, t, [100], F32, scale=scale)
+    o, l, tol, ltol, _ = attend64(c, q, t, lens, scale=scale, live=[live])
+    close(out, o, tol)
+    assert bool(((lse.double().cpu() - l).abs() <= ltol).all())
