@@ -482,7 +482,10 @@ size_t hhr_paged_workspace_size(const hhr_paged* cache);
  *   out      device, write: [B][Hq][d] of out_type (q_type or HHR_TYPE_F32).
  *   lse      device, write, nullable: f32 [B][Hq].
  *   workspace device: at least hhr_paged_workspace_size(cache) bytes.
- * Lengths and pages are read on the device, so a captured call follows them.
+ * Lengths and pages are read on the device, so a captured call follows them;
+ * lens and table must not change while the call runs.  A call whose lengths
+ * changed under it ends with outputs of no meaning, and its workspace has to be
+ * zero-filled again before the next one.
  * Supported: B * Hq < 2^31, B * Hq * table_cols * page < 2^40.  scale: any
  * finite value.  A logit of -inf leaves its token out; other non-finite values
  * among a sequence's tokens make its outputs non-finite.

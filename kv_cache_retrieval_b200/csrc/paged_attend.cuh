@@ -46,35 +46,9 @@
 
 #include "hhr_internal.cuh"
 #include "paged_common.cuh"
+#include "paged_tiles.cuh"
 
 namespace hhr {
-
-constexpr int kPagedMaxGrid = 160;   // CTAs that take part in a call (one per SM)
-constexpr int kPagedMaxWarps = 12;   // warps of a CTA
-
-struct PagedArgs {
-  const void* q;
-  const void* K;
-  const void* V;
-  const int32_t* table;
-  const int32_t* lens;
-  void* out;
-  float* lse;
-  uint32_t* status;
-  uint32_t* counters;          // [kPagedMaxGrid]: states that arrived for the unit a CTA began
-  float* parts;                // [kPagedMaxGrid][2]: joined states of a CTA's first and last unit
-  float* firsts;               // [kPagedMaxGrid][kPagedMaxWarps]: states of the units that a warp ends and did not begin
-  int64_t q_seq;                                              // elements
-  int64_t k_page, k_head, k_tok, v_page, v_head, v_tok;       // bytes
-  float scale_log2, v_scale;   // |scale| k_scale log2(e)
-  uint32_t flip;               // the signs of two 16-bit values if the scale is negative: the queries take it
-  int B, Hq, Hkv, page, n_pages, table_cols, table_stride, window, out_f32;
-  int r, chunk, chunks;        // query heads of a KV head, of a unit (at most 8 NT), and units of a KV head
-  int state;                   // floats of a state
-  uint32_t page_magic;         // n / page = (umulhi(n, magic) + n) >> shift for n < 2^31
-  int page_shift;
-  int min_tiles;               // a warp takes at least that many
-};
 
 // Floats of a state: a row of d sums of each head, then its maximum and weight sum (rows of d + 4 floats fall on
 // different banks).
@@ -109,43 +83,9 @@ struct PagedShape {
   static_assert(kSmem <= 226 * 1024, "shared memory of a CTA");
 };
 
-// Tiles of a sequence: [first, end).
-struct TileRange {
-  int lo, len, first, end;
-};
-
-template <int kTokens>
-__device__ __forceinline__ TileRange tile_range(const PagedArgs& a, int b) {
-  TileRange t;
-  t.len = a.lens[b];
-  if (t.len < 0 || t.len > a.table_cols * a.page) t.len = 0;
-  t.lo = a.window ? max(0, t.len - a.window) : 0;
-  t.first = t.lo / kTokens;
-  t.end = static_cast<int>((static_cast<uint32_t>(t.len) + (kTokens - 1)) / kTokens);
-  return t;
-}
-
 __device__ __forceinline__ int page_of(const PagedArgs& a, int n) {
   return static_cast<int>((__umulhi(static_cast<uint32_t>(n), a.page_magic) + static_cast<uint32_t>(n)) >> a.page_shift);
 }
-
-// A tile of the call: sequence, unit of the sequence, tile of the unit.
-struct TileCursor {
-  TileRange t;
-  int b, u, at;
-  template <int kTokens>
-  __device__ __forceinline__ void next(const PagedArgs& a, int units) {   // the next tile has to exist
-    if (++at < t.end) return;
-    if (++u == units) {
-      u = 0;
-      while (b + 1 < a.B) {
-        t = tile_range<kTokens>(a, ++b);
-        if (t.first < t.end) break;
-      }
-    }
-    at = t.first;
-  }
-};
 
 // An open state: one of several of its unit.
 struct OpenState {
@@ -437,19 +377,10 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
                                      : max(int64_t{1}, max(int64_t{1}, fill / max(int64_t{1}, n_units)) * n_units));
   const int n_active = static_cast<int>(min(static_cast<int64_t>(kWarps), max(int64_t{1}, total / G)));
   const int c = blockIdx.x;
-  // Warp i of them takes [first_of(i), first_of(i + 1)), a tile at least (the host bounds total * n_warps).
-  const uint32_t n_warps = G * n_active;
-  const int64_t quot = total >> 32 ? total / n_warps : static_cast<int64_t>(static_cast<uint32_t>(total) / n_warps);
-  const uint32_t rem = static_cast<uint32_t>(total - quot * n_warps);
-  const auto first_of = [&](uint32_t i) {
-    i = min(i, n_warps);
-    return quot * i + rem * i / n_warps;
-  };
-  const auto cta_of = [&](int64_t x) {   // of the warp whose range holds x: the last with total * i / n_warps <= x
-    return static_cast<int>((static_cast<uint64_t>(x + 1) * n_warps - 1) / static_cast<uint64_t>(total)) / n_active;
-  };
-  const int64_t f0 = first_of(c * n_active), f1 = first_of((c + 1) * n_active);
-  const int64_t w0 = first_of(c * n_active + warp), w1 = warp < n_active ? first_of(c * n_active + warp + 1) : w0;
+  // (a tile at least for each warp: the host bounds total * n_warps)
+  const TileDeal deal(total, G, n_active);
+  const int64_t f0 = deal.first_of(c * n_active), f1 = deal.first_of((c + 1) * n_active);
+  const int64_t w0 = deal.first_of(c * n_active + warp), w1 = warp < n_active ? deal.first_of(c * n_active + warp + 1) : w0;
 
   if (w0 < w1) {
     // ---- where w0 lies: the last run that begins at or before it, then the sequence
@@ -472,11 +403,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
         if (w0 < (pre + n) * units || seg.b + 1 >= a.B) break;
         pre += n;
       }
-      // (in range whatever `lens` holds by now: a caller that writes it during the call gets wrong rows, not a fault)
-      const int n = max(1, seg.t.end - seg.t.first);
-      const int64_t off = min(max(int64_t{0}, w0 - pre * units), static_cast<int64_t>(n) * units - 1);
-      seg.u = static_cast<int>(static_cast<uint64_t>(off) >> 32 ? off / n : static_cast<uint32_t>(off) / static_cast<uint32_t>(n));
-      seg.at = seg.t.first + static_cast<int>(off - static_cast<int64_t>(seg.u) * n);
+      seg.place(w0 - pre * units, units);
     }
 
     // ---- loads
@@ -585,9 +512,8 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
       const int g_kv = seg.u / a.chunks, first_head = (seg.u - g_kv * a.chunks) * a.chunk;
       const int heads = min(a.chunk, a.r - first_head);
       const int head0 = g_kv * a.r + first_head;
-      const int64_t x0 = f - (seg.at - seg.t.first), x1 = x0 + (seg.t.end - seg.t.first);
-      const bool began = f == x0, ends = x1 <= w1;
-      int left = static_cast<int>((ends ? x1 : w1) - f);
+      const UnitSpan span(seg, f, w1);
+      int left = span.left;
 
       // Queries: lane (g, t4) holds elements 2 t4, 2 t4 + 1 and 8 + 2 t4, 9 + 2 t4 of every 16 of head g; with 8-bit keys
       // 4 t4 .. 4 t4 + 3, the order in which the bytes of a row fill their fragments.
@@ -823,7 +749,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(~0u, l[n][e], w);
-      if (began && ends) {
+      if (span.began && span.ends) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -867,7 +793,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
             }
             if (g == 0) *reinterpret_cast<float2*>(row + D) = make_float2(paged_quarter(m[n][e], sc[n][e]), l[n][e]);
           }
-        if (lane == 0) s_open[2 * warp + last] = {x0, x1, seg.b, seg.u};
+        if (lane == 0) s_open[2 * warp + last] = {span.x0, span.x1, seg.b, seg.u};
       }
       if (f == w1) break;
       seg.at = seg.t.end - 1;
@@ -891,12 +817,12 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
     const bool begins = x1 != 0 && (!ahead || x0_ahead != x0);   // the first state of its unit
     const uint32_t all = __ballot_sync(~0u, begins);
     if (lane == 0) {
-      s_joins = __popc(all);
+      s_joins = min(__popc(all), kWarps + 1);
       s_side[0] = s_side[1] = -1;
     }
     __syncwarp();
-    if (begins) {
-      const int k = __popc(all & ((1u << lane) - 1));
+    const int k = __popc(all & ((1u << lane) - 1));
+    if (begins && k <= kWarps) {   // (more units than that: lengths that changed during the call)
       const uint32_t behind = all & ~((2u << lane) - 1);
       const uint32_t upto = open & (behind ? (1u << (__ffs(behind) - 1)) - 1 : ~0u);
       const int i1 = 31 - __clz(upto), wa = lane >> 1, wb = i1 >> 1;
@@ -930,8 +856,8 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
       int n = 0;
       if (k >= 0) {
         Join& j = s_join[k];
-        const int c0 = cta_of(j.x0);
-        n = cta_of(j.x1 - 1) - c0 + 1;
+        const int c0 = deal.cta_of(j.x0, gridDim.x);
+        n = max(1, deal.cta_of(j.x1 - 1, gridDim.x) - c0 + 1);
         uint32_t* const count = a.counters + c0;
         uint32_t old;
         asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(count) : "memory");

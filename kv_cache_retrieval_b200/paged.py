@@ -148,7 +148,8 @@ class HHRPagedCache:
         each sequence, or the last `window` of them; into out (dtype or float32;
         a new tensor of dtype if None) and lse (float32 [B, q_heads], optional).
         scale: 1/sqrt(head_dim) if None.  workspace (new_workspace): needed by calls that may
-        run at the same time as another one on this cache.  A serving call: it has no gradient."""
+        run at the same time as another one on this cache.  lens and table must not change while the call runs (hhr.h,
+        hhr_paged_attend).  A serving call: it has no gradient."""
         index = self._index
         desc, rows = self._table(table)
         q_B, q_seq = self._rows("q", q, self._Hq)
