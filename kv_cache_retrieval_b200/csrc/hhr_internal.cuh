@@ -4,6 +4,7 @@
 #include <cstddef>
 #include <atomic>
 #include <cstdint>
+#include <mutex>
 
 #include <cuda_runtime.h>
 
@@ -157,19 +158,20 @@ inline __host__ __device__ DecodeSmem decode_smem(int NP, int C, int bits, int r
 // Raises a kernel's dynamic shared-memory limit to at least `bytes` on the
 // current device, calling cudaFuncSetAttribute only when the limit grows
 // (one record per kernel and device: `raised` must be a zero-initialised
-// static array of kMaxDevices entries).
+// static array of kMaxDevices entries).  Limit and record change together: of
+// two threads' first calls the smaller size never comes last.
 constexpr int kMaxDevices = 64;
 inline cudaError_t ensure_smem_limit(const void* kernel, size_t bytes, std::atomic<size_t>* raised) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < kMaxDevices && raised[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+  const bool kept = dev < kMaxDevices;
+  if (kept && raised[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+  static std::mutex setting;
+  const std::lock_guard<std::mutex> lock(setting);
+  if (kept && raised[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess && dev < kMaxDevices) {
-    size_t cur = raised[dev].load(std::memory_order_relaxed);
-    while (cur < bytes && !raised[dev].compare_exchange_weak(cur, bytes, std::memory_order_release)) {
-    }
-  }
+  if (e == cudaSuccess && kept) raised[dev].store(bytes, std::memory_order_release);
   return e;
 }
 
