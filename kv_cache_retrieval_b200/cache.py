@@ -54,11 +54,11 @@ class HHRCache:
         if self._paged is None:
             d = self.dims
             self._paged = (HHRPagedCache(q_heads=d.Hq, kv_heads=d.Hkv, page=d.n_cap, head_dim=d.d, K=self.K, V=self.V),
-                           torch.arange(d.B, dtype=torch.int32, device=self.device).view(d.B, 1))
+                           torch.arange(d.B, dtype=torch.int32, device=self.K.device).view(d.B, 1))
         return self._paged
 
     def append(self, k, v, n_begin, *, q=None, freqs=None, interleaved=False, mscale=1.0):
-        """Takes tokens n_begin .. n_begin + n of every sequence on the current stream: k, v bf16
+        """Takes tokens n_begin .. n_begin + n of every sequence on the current stream of the cache's device: k, v bf16
         [batch, n, kv_heads, head_dim] as the projection leaves them.  Their keys are rotated by their places
         (freqs: rope_freqs; None: as they are), stored with the values, and encoded.  Returns q [batch, n, q_heads,
         head_dim] rotated by the same places, or None."""
@@ -70,12 +70,13 @@ class HHRCache:
         n = k.shape[1]
         if n_begin < 0 or n_begin + n > d.n_cap:
             raise ValueError(f"tokens {n_begin} .. {n_begin + n} of a capacity of {d.n_cap}")
-        pos = torch.arange(n_begin, n_begin + n, dtype=torch.int32, device=self.device).repeat(d.B)
-        seq = table.expand(d.B, n).reshape(-1)
-        rows = [None if t is None else t.flatten(0, 1) for t in (k, v, q)]
-        out = paged.append(rows[0], rows[1], pos, table, seq=seq, q=rows[2], freqs=freqs, interleaved=interleaved,
-                           mscale=mscale)
-        self.encode(n_begin, n_begin + n)
+        with torch.cuda.device(self.K.device):      # the encoding goes to that device's current stream, too
+            pos = torch.arange(n_begin, n_begin + n, dtype=torch.int32, device=self.K.device).repeat(d.B)
+            seq = table.expand(d.B, n).reshape(-1)
+            rows = [None if t is None else t.flatten(0, 1) for t in (k, v, q)]
+            out = paged.append(rows[0], rows[1], pos, table, seq=seq, q=rows[2], freqs=freqs, interleaved=interleaved,
+                               mscale=mscale)
+            self.encode(n_begin, n_begin + n)
         return None if q is None else out.view(q.shape)
 
     # -- decode -------------------------------------------------------------

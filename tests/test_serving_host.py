@@ -1,0 +1,32 @@
+"""The host side of the serving calls, without a GPU: devices, what is kept between calls, sizes that do not fit."""
+import contextlib
+
+import pytest
+import torch
+
+import kv_cache_retrieval_b200 as hhr
+from kv_cache_retrieval_b200 import _binding, build as kbuild
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    kbuild.build()
+
+
+def test_the_retrieval_caches_append_stays_on_its_device(monkeypatch):
+    """Both halves of the append, the store and the encoding, run with the cache's device current."""
+    c = hhr.HHRCache(batch=1, q_heads=4, kv_heads=2, capacity=64, P=2, k=8, device="cpu")
+    current, seen = ["cuda:0"], []
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], str(d)
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(hhr.HHRPagedCache, "append", lambda self, *a, **k: seen.append(("append", current[0])))
+    monkeypatch.setattr(_binding, "hhr_encode_keys", lambda *a, **k: seen.append(("encode", current[0])))
+    k = torch.zeros(1, 3, 2, 128, dtype=torch.bfloat16)
+    c.append(k, k, 0)
+    assert seen == [("append", "cpu"), ("encode", "cpu")] and current == ["cuda:0"]
