@@ -46,7 +46,8 @@ _rotations = {}
 
 
 def rotation(rot, flags, mscale):
-    """A reference to an hhr_rotation (kept: the few a program uses are made once)."""
+    """A reference to an hhr_rotation (kept by value: the few a program uses are made once)."""
+    mscale = float(mscale)    # a tensor would be its own key, whatever it holds by then
     r = _rotations.get((rot, flags, mscale))
     if r is None:
         if len(_rotations) >= 64:
@@ -96,7 +97,7 @@ def rope(x, positions, freqs, *, interleaved=False, mscale=1.0, out=None):
     index = x.get_device()
     check_vector("positions", positions, torch.int32, shape[0], index)
     check_vector("freqs", freqs, torch.float64, freqs.numel(), index)
-    flags = B.HHR_ROPE_INTERLEAVED if interleaved else 0
+    flags, mscale = B.HHR_ROPE_INTERLEAVED if interleaved else 0, float(mscale)   # (the gradient takes this value, too)
     if x.requires_grad and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out= has no gradient: call without it, or on x.detach()")

@@ -30,3 +30,14 @@ def test_the_retrieval_caches_append_stays_on_its_device(monkeypatch):
     k = torch.zeros(1, 3, 2, 128, dtype=torch.bfloat16)
     c.append(k, k, 0)
     assert seen == [("append", "cpu"), ("encode", "cpu")] and current == ["cuda:0"]
+
+
+@pytest.mark.parametrize("make", [torch.tensor, lambda x: torch.tensor([x], dtype=torch.float64)])
+def test_a_scale_that_changes_in_place_is_read_again(make):
+    """Rotations are kept by their values, not by the object that held one."""
+    from kv_cache_retrieval_b200.rope import rotation
+    m = make(1.25)
+    assert rotation(64, 0, m)._obj.mscale == 1.25
+    m.fill_(0.5)
+    assert rotation(64, 0, m)._obj.mscale == 0.5
+    assert rotation(64, 0, 0.5) is rotation(64, 0, m)
