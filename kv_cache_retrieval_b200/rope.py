@@ -4,6 +4,7 @@ from __future__ import annotations
 import ctypes as C
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _binding as B
 
@@ -69,28 +70,44 @@ def _rotate(x, positions, freqs, flags, mscale, out):
     return out
 
 
+def _followed(x):
+    """Whether a derivative of x is asked for: a gradient, or the tangent of a dual tensor."""
+    return (x.requires_grad and torch.is_grad_enabled()) or \
+        (forward_ad._current_level >= 0 and forward_ad.unpack_dual(x).tangent is not None)
+
+
+def _turn(x, positions, freqs, flags, mscale):
+    """x rotated, with the derivatives that are asked for."""
+    if _followed(x):
+        return _Rope.apply(x, positions, freqs, flags, mscale)
+    return _rotate(x, positions, freqs, flags, mscale, x.new_empty(x.shape))
+
+
 class _Rope(torch.autograd.Function):
+    # The rotation is linear: the tangent is the rotation of x's tangent, the gradient the transposed rotation, and the
+    # derivatives of these are again the two.
     @staticmethod
     def forward(ctx, x, positions, freqs, flags, mscale):
         ctx.save_for_backward(positions, freqs)
+        ctx.save_for_forward(positions, freqs)
         ctx.how = flags, mscale
         return _rotate(x, positions, freqs, flags, mscale, x.new_empty(x.shape))
 
     @staticmethod
     def backward(ctx, g):
-        # the Jacobian of a rotation is the rotation: its transpose gives the gradient, and the gradient's gradient again
         positions, freqs = ctx.saved_tensors
         flags, mscale = ctx.how
-        flags ^= B.HHR_ROPE_TRANSPOSE
-        if g.requires_grad and torch.is_grad_enabled():
-            return _Rope.apply(g, positions, freqs, flags, mscale), None, None, None, None
-        return _rotate(g, positions, freqs, flags, mscale, g.new_empty(g.shape)), None, None, None, None
+        return _turn(g, positions, freqs, flags ^ B.HHR_ROPE_TRANSPOSE, mscale), None, None, None, None
+
+    @staticmethod
+    def jvp(ctx, tangent, *_):
+        return _turn(tangent, *ctx.saved_tensors, *ctx.how)
 
 
 def rope(x, positions, freqs, *, interleaved=False, mscale=1.0, out=None):
     """x [T, H, d] (bf16, fp16 or fp32; any token and head strides) with its first 2 * freqs.numel() elements
     rotated by positions[t] * freqs (hhr_rope).  positions: int32 [T]; freqs: float64 [rot/2].  Differentiable
-    with respect to x.  out: where to put the result (x itself rotates in place); not with a gradient."""
+    with respect to x, backward and forward (dual tensors).  out: where to put the result (x itself rotates in place); not with a gradient."""
     shape = x.shape
     if len(shape) != 3 or x.dtype not in _TYPES or not x.is_cuda:
         raise ValueError(f"x: expected a bf16, fp16 or fp32 CUDA tensor [T, H, d], got {x.dtype} {tuple(x.shape)} on {x.device}")
@@ -98,7 +115,7 @@ def rope(x, positions, freqs, *, interleaved=False, mscale=1.0, out=None):
     check_vector("positions", positions, torch.int32, shape[0], index)
     check_vector("freqs", freqs, torch.float64, freqs.numel(), index)
     flags, mscale = B.HHR_ROPE_INTERLEAVED if interleaved else 0, float(mscale)   # (the gradient takes this value, too)
-    if x.requires_grad and torch.is_grad_enabled():
+    if _followed(x):
         if out is not None:
             raise ValueError("out= has no gradient: call without it, or on x.detach()")
         return _Rope.apply(x, positions, freqs, flags, mscale)
