@@ -14,7 +14,7 @@ import math
 import torch
 
 from . import _binding as B
-from .rope import check_vector, on_device, rotation
+from .rope import check_vector, on_device, rotation, written
 
 _TYPES = {torch.bfloat16: B.HHR_TYPE_BF16, torch.float16: B.HHR_TYPE_F16, torch.float32: B.HHR_TYPE_F32,
           torch.float8_e4m3fn: B.HHR_TYPE_E4M3}
@@ -134,6 +134,7 @@ class HHRPagedCache:
             half = freqs.numel()
             check_vector("freqs", freqs, torch.float64, half, index)
             rot = rotation(2 * half, B.HHR_ROPE_INTERLEAVED if interleaved else 0, mscale)
+        written((self.K, self.V) if q is None else (self.K, self.V, q_out))
         st = on_device(index, B.lib().hhr_paged_append, desc, T, rows, rot, None if freqs is None else freqs.data_ptr(),
                        positions.data_ptr(), None if rope_positions is None else rope_positions.data_ptr(),
                        None if seq is None else seq.data_ptr(), table.data_ptr(), None if q is None else q.data_ptr(), q_tok,
@@ -168,6 +169,7 @@ class HHRPagedCache:
             workspace = self.workspace
         elif workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError(f"workspace: expected a contiguous tensor on {self.device}")
+        written((out,) if lse is None else (out, lse))
         st = on_device(index, B.lib().hhr_paged_attend, desc, rows, q.data_ptr(), q_seq, self.K.data_ptr(), self.V.data_ptr(),
                        table.data_ptr(), lens.data_ptr(), window, self.scale if scale is None else scale, _TYPES[out.dtype],
                        out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),

@@ -43,6 +43,11 @@ def check_vector(name, t, dtype, length, index):
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+# Tells autograd that the library writes the tensors of a tuple: a graph that saved one of them for its gradient then says
+# so, instead of taking what it holds by now.  (autograd.graph.increment_version without its own look at the argument.)
+written = torch._C._increment_version
+
+
 _rotations = {}
 
 
@@ -115,7 +120,7 @@ def rope(x, positions, freqs, *, interleaved=False, mscale=1.0, out=None):
     check_vector("positions", positions, torch.int32, shape[0], index)
     check_vector("freqs", freqs, torch.float64, freqs.numel(), index)
     flags, mscale = B.HHR_ROPE_INTERLEAVED if interleaved else 0, float(mscale)   # (the gradient takes this value, too)
-    if _followed(x):
+    if (x.requires_grad or forward_ad._current_level >= 0) and _followed(x):
         if out is not None:
             raise ValueError("out= has no gradient: call without it, or on x.detach()")
         return _Rope.apply(x, positions, freqs, flags, mscale)
@@ -125,4 +130,8 @@ def rope(x, positions, freqs, *, interleaved=False, mscale=1.0, out=None):
             (out.stride(2) != 1 and shape[2] > 1):
         raise ValueError(f"out: expected {x.dtype} {tuple(x.shape)} on {x.device} with adjacent elements of a head, "
                          f"got {out.dtype} {tuple(out.shape)} on {out.device}")
+    elif out.requires_grad and torch.is_grad_enabled():
+        raise ValueError("out= has no gradient: give it a tensor that needs none")
+    else:
+        written((out,))
     return _rotate(x, positions, freqs, flags, mscale, out)

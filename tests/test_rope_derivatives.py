@@ -40,3 +40,44 @@ def test_the_tangent_of_a_gradient_and_the_gradient_of_a_tangent():
         dy = forward_ad.unpack_dual(hhr.rope(forward_ad.make_dual(x, tangent), pos, f)).tangent
     (back,) = torch.autograd.grad(dy, tangent, g)
     check(back, g, pos, f, transpose=True)
+
+
+def test_a_saved_tensor_that_is_overwritten_is_noticed():
+    """Writes in place and into out= raise the tensor's version: a graph that saved it refuses its backward pass."""
+    f = _freqs(64)
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")
+    w = torch.ones((), device="cuda", requires_grad=True)
+    x, room = _x((4, 2, 64), torch.float32), _x((4, 2, 64), torch.float32)
+    for write in (lambda: hhr.rope(x, pos, f, out=x), lambda: hhr.rope(x, pos, f, out=room)):
+        loss = (w * x * room).sum()
+        write()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    loss = (w * x).sum()
+    hhr.rope(x, pos, f)
+    loss.backward()
+    with pytest.raises(ValueError):
+        hhr.rope(x, pos, f, out=room.requires_grad_())
+    with torch.no_grad():
+        hhr.rope(x, pos, f, out=room)
+    with torch.inference_mode():
+        hhr.rope(x, pos, f, out=torch.empty_like(x))
+
+
+def test_the_paged_calls_raise_the_versions_of_what_they_write():
+    c = hhr.HHRPagedCache(q_heads=4, kv_heads=2, pages=4, page=16, head_dim=64)
+    k = torch.zeros(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    q, out = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(1, 4, 64, device="cuda")
+    lse, table = torch.empty(1, 4, device="cuda"), torch.zeros(1, 4, dtype=torch.int32, device="cuda")
+    pos, lens = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+
+    def raised(call, *tensors):
+        before = [t._version for t in tensors]
+        call()
+        return [t._version > b for t, b in zip(tensors, before)]
+
+    assert raised(lambda: c.append(k, k, pos, table), c.K, c.V, k) == [True, True, False]
+    assert raised(lambda: c.append(k, k, pos, table, q=q, q_out=q), c.K, c.V, q) == [True] * 3
+    assert raised(lambda: c.attend(q, table, lens, out=out, lse=lse), out, lse, q, c.K) == [True, True, False, False]
+    with torch.inference_mode():      # tensors without a version
+        hhr.HHRPagedCache(q_heads=4, kv_heads=2, pages=4, page=16, head_dim=64).append(k, k, pos, table, q=q, q_out=q.clone())
