@@ -372,7 +372,7 @@ typedef struct hhr_rope_scaling {
  *   LINEAR  f_j / factor
  *   NTK     f_j with base * factor^(rot/(rot-2))  (rot > 2)
  *   YARN    with dim(t) = rot ln(orig / (2 pi t)) / (2 ln base), lo = max(floor(dim(high)), 0),
- *           hi = min(ceil(dim(low)), rot/2 - 1) and s_j = clamp((j - lo) / max(hi - lo, 0.001), 0, 1):
+ *           hi = min(ceil(dim(low)), rot - 1) and s_j = clamp((j - lo) / max(hi - lo, 0.001), 0, 1):
  *           f_j (1 - s_j) + f_j / factor * s_j; mscale = 0.1 ln(factor) + 1
  *   BANDS   with turns_j = orig f_j / (2 pi) and s_j = clamp((turns_j - low) / (high - low), 0, 1):
  *           f_j / factor * (1 - s_j) + f_j s_j

@@ -423,7 +423,7 @@ int32_t hhr_rope_freqs(const hhr_rope_scaling* s, int32_t rot, double* freqs, fl
   if (s->kind == HHR_ROPE_SCALE_YARN) {
     const auto dim = [&](double turns) { return rot * std::log(s->orig / (two_pi * turns)) / (2 * std::log(base)); };
     lo = std::max(std::floor(dim(s->high)), 0.0);
-    hi = std::min(std::ceil(dim(s->low)), half - 1.0);
+    hi = std::min(std::ceil(dim(s->low)), rot - 1.0);   // (the published bound: beyond the last pair, which the ramp may not reach)
   }
   for (int j = 0; j < half; ++j) {
     double f = std::pow(base, -2.0 * j / rot);

@@ -13,7 +13,19 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: full-size workload (minutes)")
 
 
+# Cases whose own value is wrong, with the reason: they have to fail (strict), and the right value has a test of its own.
+WRONG_VALUES = {
+    "test_rope.py::test_frequencies_follow_the_formulas[yarn-4.0-32768-1.0-32.0-4]":
+        "clamps the ramp's end at rot/2 - 1 = 1 where the published formula has rot - 1 = 3: dim(1) = 1.304 gives hi = 2, "
+        "the second pair s = 1/2 and the frequency 8.839e-4, not 3.536e-4 (test_rope_frequencies.py)",
+}
+
+
 def pytest_collection_modifyitems(config, items):
+    for item in items:
+        for name, why in WRONG_VALUES.items():
+            if item.nodeid.endswith(name):
+                item.add_marker(pytest.mark.xfail(reason=why, strict=True))
     try:
         import torch
         has_gpu = torch.cuda.is_available()
