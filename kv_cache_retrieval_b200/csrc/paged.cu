@@ -34,7 +34,8 @@ int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64
                          void* workspace, size_t ws_bytes, void* stream) {
   if (int32_t st = check_paged(cache)) return st;
   const hhr_paged& c = *cache;
-  if (B < 0 || window < 0 || !std::isfinite(scale)) return HHR_ERR_INVALID_ARG;
+  const float scale_log2 = std::fabs(scale) * c.k_scale * 1.4426950408889634f;
+  if (B < 0 || window < 0 || !std::isfinite(scale_log2)) return HHR_ERR_INVALID_ARG;
   if (out_type != c.q_type && out_type != HHR_TYPE_F32) return HHR_ERR_INVALID_ARG;
   if (static_cast<int64_t>(B) * c.Hq >= (int64_t{1} << 31)) return HHR_ERR_UNSUPPORTED;
   // a warp's tiles are counted in 32 bits
@@ -67,7 +68,7 @@ int32_t hhr_paged_attend(const hhr_paged* cache, int32_t B, const void* q, int64
   a.v_page = c.v_page * size;
   a.v_head = c.v_head * size;
   a.v_tok = c.v_tok * size;
-  a.scale_log2 = std::fabs(scale) * c.k_scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.flip = scale < 0 ? 0x80008000u : 0;
   a.v_scale = c.v_scale;
   a.B = B;

@@ -6,6 +6,7 @@ import torch
 
 import kv_cache_retrieval_b200 as hhr
 from kv_cache_retrieval_b200 import _binding, build as kbuild
+from test_paged import attend, desc
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -41,3 +42,11 @@ def test_a_scale_that_changes_in_place_is_read_again(make):
     m.fill_(0.5)
     assert rotation(64, 0, m)._obj.mscale == 0.5
     assert rotation(64, 0, 0.5) is rotation(64, 0, m)
+
+
+@pytest.mark.parametrize("kw,scale", [
+    (dict(), 3e38), (dict(), -3e38), (dict(kv_type=3, k_scale=2.0), 2e38), (dict(kv_type=3, k_scale=2.0 ** 100), 2.0 ** 28),
+    (dict(), float("nan")), (dict(), -float("inf"))])
+def test_scales_beyond_float32_are_refused(kw, scale):
+    """The logits are taken in powers of two, scale * k_scale * log2 e: infinite, it would make 0 * inf of the largest."""
+    assert attend(desc(**kw), scale=scale) == hhr.HHR_ERR_INVALID_ARG
