@@ -14,7 +14,7 @@ import math
 import torch
 
 from . import _binding as B
-from .rope import check_vector, on_device, rotation, written
+from .rope import check_vector, fits, on_device, rotation, written
 
 _TYPES = {torch.bfloat16: B.HHR_TYPE_BF16, torch.float16: B.HHR_TYPE_F16, torch.float32: B.HHR_TYPE_F32,
           torch.float8_e4m3fn: B.HHR_TYPE_E4M3}
@@ -55,6 +55,7 @@ class HHRPagedCache:
             raise ValueError(f"kv_dtype must be {dtype} or float8_e4m3fn, got {K.dtype}")
         self.K, self.V, self.device, self.dtype = K, V, K.device, dtype
         self.scale = 1.0 / math.sqrt(head_dim)
+        fits(q_heads, pages)
         h, t = (1, 2) if layout == "head" else (2, 1)
         self.desc = B.hhr_paged(q_heads, kv_heads, head_dim, page, pages, 1, 1, _TYPES[dtype], _TYPES[K.dtype],
                                 k_scale, v_scale, 0, *(s.stride(i) for s in (K, V) for i in (0, h, t)))
@@ -82,7 +83,7 @@ class HHRPagedCache:
         desc = self._descs.get((cols, stride))
         if desc is None:   # never changed after this: another thread's call may be reading it
             desc = B.hhr_paged.from_buffer_copy(self.desc)
-            desc.table_cols, desc.table_stride = cols, stride
+            desc.table_cols, desc.table_stride = fits(cols, stride)
             if len(self._descs) >= 64:
                 self._descs.clear()
             desc = self._descs[cols, stride] = C.byref(desc)
@@ -97,6 +98,8 @@ class HHRPagedCache:
         row, head, one = t.stride()
         if one != 1 or (heads > 1 and head != d):
             raise ValueError(f"{name}: a token's heads have to be adjacent")
+        if shape[0] >> 31:
+            fits(shape[0])
         return shape[0], row
 
     def append(self, k, v, positions, table, *, seq=None, q=None, q_out=None, freqs=None, rope_positions=None,
@@ -165,6 +168,8 @@ class HHRPagedCache:
         if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (rows, self._Hq) or
                                 lse.get_device() != index or not lse.is_contiguous()):
             raise ValueError(f"lse: expected a contiguous float32 tensor [{rows}, {self._Hq}] on {self.device}")
+        if window >> 31:      # no sequence is that long
+            window = (1 << 31) - 1 if window > 0 else -1
         if workspace is None:
             workspace = self.workspace
         elif workspace.get_device() != index or not workspace.is_contiguous():

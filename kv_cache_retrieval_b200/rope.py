@@ -43,6 +43,13 @@ def check_vector(name, t, dtype, length, index):
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def fits(*sizes):
+    """The sizes, which the library takes as int32: ctypes would drop the bits beyond."""
+    if any(n >> 31 for n in sizes):
+        raise ValueError(f"sizes of 2^31 and more: {sizes}")
+    return sizes
+
+
 # Tells autograd that the library writes the tensors of a tuple: a graph that saved one of them for its gradient then says
 # so, instead of taking what it holds by now.  (autograd.graph.increment_version without its own look at the argument.)
 written = torch._C._increment_version
@@ -68,6 +75,8 @@ def _rotate(x, positions, freqs, flags, mscale, out):
     if sx[2] != 1 and d > 1:
         x = x.contiguous()
         sx = x.stride()
+    if T >> 31 or H >> 31:
+        fits(T, H)
     st = on_device(x.get_device(), B.lib().hhr_rope, T, H, d, _TYPES[x.dtype], rotation(2 * freqs.shape[0], flags, mscale),
                    freqs.data_ptr(), positions.data_ptr(), x.data_ptr(), sx[0], sx[1], out.data_ptr(), so[0], so[1])
     if st:

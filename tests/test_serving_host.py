@@ -1,5 +1,6 @@
 """The host side of the serving calls, without a GPU: devices, what is kept between calls, sizes that do not fit."""
 import contextlib
+import sys
 
 import pytest
 import torch
@@ -50,3 +51,31 @@ def test_a_scale_that_changes_in_place_is_read_again(make):
 def test_scales_beyond_float32_are_refused(kw, scale):
     """The logits are taken in powers of two, scale * k_scale * log2 e: infinite, it would make 0 * inf of the largest."""
     assert attend(desc(**kw), scale=scale) == hhr.HHR_ERR_INVALID_ARG
+
+
+def test_sizes_beyond_int32_are_not_cut_off(monkeypatch):
+    """The library takes int32; ctypes drops what is beyond.  (Tensors without memory: nothing is called.)"""
+    paged, rope = (sys.modules["kv_cache_retrieval_b200." + m] for m in ("paged", "rope"))
+    calls = []
+    monkeypatch.setattr(paged, "on_device", lambda index, fn, *args: calls.append(args) or 0)
+    monkeypatch.setattr(rope, "on_device", lambda index, fn, *args: calls.append(args) or 0)
+    c = hhr.HHRPagedCache(q_heads=8, kv_heads=2, pages=4, head_dim=64, device="cpu")
+    table, lens = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    q = torch.zeros(3, 8, 64, dtype=torch.bfloat16)
+    for window, passed in ((0, 0), (7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1)):
+        c.attend(q, table, lens, window=window)
+        assert calls.pop()[8] == passed
+    c.attend(q, table, lens, window=-2 ** 32)      # refused by the library
+    assert calls.pop()[8] == -1
+    many = 2 ** 32 + 3
+    k = torch.empty(many, 2, 64, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="2\\^31"):
+        c.append(k, k, torch.empty(many, dtype=torch.int32, device="meta"), table)
+    with pytest.raises(ValueError, match="2\\^31"):
+        c.attend(q, torch.empty(3, many, dtype=torch.int32, device="meta"), lens)
+    x = torch.empty(many, 1, 2, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="2\\^31"):
+        rope._rotate(x, torch.empty(many, dtype=torch.int32, device="meta"), torch.empty(1, device="meta"), 0, 1.0, x)
+    with pytest.raises(ValueError, match="2\\^31"):
+        hhr.HHRPagedCache(q_heads=2 ** 32 + 8, kv_heads=2, pages=4, head_dim=64, device="cpu")
+    assert not calls
