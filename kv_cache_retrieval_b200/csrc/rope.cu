@@ -353,7 +353,10 @@ cudaError_t launch_rows(RopeArgs& a, cudaStream_t stream) {
   a.places = a.d / (2 * V);
   const int step = kRopeThreads / a.places;      // groups of a block
   const int64_t rows = static_cast<int64_t>(a.T) * (a.H + 2 * a.Hkv);
-  const int U = a.H + 2 * a.Hkv >= 4 && rows >= static_cast<int64_t>(step) * 4 * 592 ? 4 : 1;
+  int dev = 0, sms = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return e;
+  const int U = a.H + 2 * a.Hkv >= 4 && rows >= static_cast<int64_t>(step) * 4 * (4 * sms) ? 4 : 1;
   a.q_groups = (a.H + U - 1) / U;
   a.kv_groups = (a.Hkv + U - 1) / U;
   a.groups = a.q_groups + 2 * a.kv_groups;
@@ -364,9 +367,6 @@ cudaError_t launch_rows(RopeArgs& a, cudaStream_t stream) {
                       2 * static_cast<size_t>(a.tokens_block) * (a.rot * sizeof(float) + 2 * sizeof(int64_t));
   static std::atomic<size_t> raised[2][kMaxDevices];
   const auto kern = U == 4 ? rope_kernel<TI, TC, V, 4, kCache> : rope_kernel<TI, TC, V, 1, kCache>;
-  int dev = 0, sms = 0;
-  if (cudaError_t e = cudaGetDevice(&dev)) return e;
-  if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return e;
   if (smem > 48 * 1024)
     if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem, raised[U == 4])) return e;
   const dim3 grid(static_cast<unsigned>(U == 4 && V > 1 ? std::min(a.tiles, sms * 3) : a.tiles));
