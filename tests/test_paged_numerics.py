@@ -109,3 +109,67 @@ def test_lowest_values_at_any_scale(scale):
     o, l, tol, ltol, _ = attend64(c, q, t, lens, scale=scale, live=[live])
     close(out, o, tol)
     assert bool(((lse.double().cpu() - l).abs() <= ltol).all())
+
+
+# ---------------------------------------------------------------- float32 outputs
+
+def bits16(w, dtype, terms):
+    """w as a sum of 16-bit terms, each rounding what those before it leave."""
+    out = torch.zeros_like(w)
+    for _ in range(terms):
+        out = out + (w - out).to(dtype).double()
+    return out
+
+
+@pytest.mark.parametrize("dtype,kv", TYPES)
+@pytest.mark.parametrize("n", [2, 3, 9])
+def test_weights_of_float32_outputs(dtype, kv, n):
+    """A few tokens of nearly equal weights: the output has the roundings of its weights and hardly any of sums.  With
+    e the logits' error: 4 e (two weights, over and under the line); ex2 of each, 2^-22, and the fp16 lift's rounding,
+    2^-21.5, twice: 2^-20; the terms' rest, 2^-22; three 16-bit products, each a sum that may lose 2^-22; the sum of the
+    weights, its inverse and the last product, 2^-22.  In all 4 e + 2^-20 + 5 2^-22.  Weights of one term less are
+    further off than that (of two or three tokens; in nine they average out)."""
+    c, q, t = make(8, 16, 2, 128, 16, 1, dtype=dtype, kv=kv, scales=(0.25, 2.0 ** -6) if kv == E4 else (1.0, 1.0), hot=False)
+    scales = (c.desc.k_scale, c.desc.v_scale)
+    q = (q.float() / 512).to(dtype)
+    out, _, lens = attend(c, q, t, [n] * 8, F32)
+    # the definition and, as a planted mistake, the same with coarser weights
+    k = c.K.float()[t[:, 0].long()].double().cpu()[:, :, :n] * scales[0]
+    v = c.V.float()[t[:, 0].long()].double().cpu()[:, :, :n] * scales[1]
+    qd = q.double().cpu().view(8, 2, 8, 128)
+    x = torch.einsum("bghd,bgnd->bghn", qd, k) / math.sqrt(128)
+    e = (torch.einsum("bghd,bgnd->bghn", qd.abs(), k.abs()) / math.sqrt(128)).amax(-1, keepdim=True) * 132 * 2.0 ** -24
+    w = torch.exp(x - x.amax(-1, keepdim=True))
+    mix = lambda a: torch.einsum("bghn,bgnd->bghd", a, v) / w.sum(-1, keepdim=True)  # noqa: E731
+    o = mix(w)
+    tol = (4 * e + 2.0 ** -20 + 5 * 2.0 ** -22) * torch.einsum("bghn,bgnd->bghd", w, v.abs()) / w.sum(-1, keepdim=True)
+    close(out, o.reshape(8, 16, 128), tol.reshape(8, 16, 128))
+    products = BF if kv == BF else FP16
+    if n > 3:
+        return
+    coarse = mix(bits16(w, products, 2 if products == BF else 1))
+    assert int(((coarse - o).abs() > tol + 2.0 ** -24 * o.abs()).sum()) > 100
+
+
+def test_sums_of_float32_outputs():
+    """Units that are one warp's each, long enough for their running sums to show: products of a tile are added by float32
+    additions, n / 16 of them for the output and as many for the sum of the weights (and one more within a tile), each off
+    by 2^-24 of what has been summed so far, on average half of the end: 2^-24 n / 16 + 2^-24 n / 32 in all, on top of the
+    above.  Sums that stay in the tensor cores from tile to tile lose several times as much, all in one direction."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    Hkv, d, n = 8, 64, 4096
+    B = -(-12 * min(sms, 160) // Hkv)
+    g = torch.Generator().manual_seed(3)
+    K = (torch.randn(n // 16, Hkv, 16, d, generator=g) / 8).to(BF).cuda()
+    V = (torch.rand(n // 16, Hkv, 16, d, generator=g) + 0.5).to(BF).cuda()
+    c = hhr.HHRPagedCache(q_heads=Hkv, kv_heads=Hkv, page=16, head_dim=d, K=K, V=V)
+    q = (torch.randn(B, Hkv, d, generator=g) / 8).to(BF).cuda()
+    table = torch.arange(n // 16, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()   # all share their pages
+    out, _, _ = attend(c, q, table, [n] * B, F32)
+    k, v = (p.double().cpu().transpose(1, 2).reshape(n, Hkv, d) for p in (K, V))
+    x = torch.einsum("bhd,nhd->bhn", q.double().cpu(), k) / 8
+    e = (torch.einsum("bhd,nhd->bhn", q.double().cpu().abs(), k.abs()) / 8).amax(-1)[..., None] * 68 * 2.0 ** -24
+    w = torch.softmax(x, -1)
+    o = torch.einsum("bhn,nhd->bhd", w, v)
+    tol = (4 * e + 2.0 ** -20 + 5 * 2.0 ** -22 + 2.0 ** -24 * (n / 16 + n / 32)) * o
+    close(out, o, tol)
