@@ -26,10 +26,11 @@
 // and O^T += V^T P^T, float32 sums.  P is a sum of 16-bit terms, by what the output's own rounding hides: three of bf16
 // for a float32 output (2^-25), two of bf16 for a bf16 output (2^-17; one, 2^-8, would show; three change 0.3 % of the
 // values by a step and cost 8 % in groups of 12 to 24 heads), two of fp16 (2^-22; one, 2^-11, is an eighth of a bf16
-// output's rounding, but moves 6 % of its values a step from the float32 result's rounding where two move 0.1 %; it
-// takes 53 us where two take 59, 16 heads, 8-bit cache).  The tensor cores' own sums
-// lose up to a unit of their last place at every step: for a float32 output a tile's product is a sum of its own, added
-// by an ordinary addition (128K tokens: relative error 1.9e-6 without, 5e-7 with it).  8-bit elements become fp16 in
+// output's rounding, but moves 6 % of its values a step from the float32 result's rounding where two move 0.1 %; it takes
+// 53 us where two take 59, 16 heads, 8-bit cache).  The tensor cores' own sums lose up to a few units of their last place
+// at every step, all in one direction: a tile's product is a sum of its own, added by an ordinary addition (a warp's unit
+// of 64K tokens: relative error 4e-6; in the tensor cores 2.9e-4, half a step of fp16; groups of up to 8 heads take the
+// same time, 16 heads of an 8-bit cache 61 us for 60, 24 heads of bf16 54 for 51).  8-bit elements become fp16 in
 // registers, exactly; bf16 queries of an 8-bit cache become fp16 after a power of two per row that makes their largest
 // element about 2^14 (elements below 2^-28 of it lose bits).  mma.sync and not tcgen05: a tile is 16 tokens of one warp,
 // whose P never leaves its registers; the tensor pipe has room to spare (busy 18 % at 128K), and a 128-row tile with its
@@ -37,7 +38,7 @@
 //
 // Measured (B200, captured passes): 1 x 128K, 8 KV heads of 128, bf16: 86 us, 6.25 TB/s (0.97 of the copy bandwidth);
 // 8 x 64K: 305 us, 7.0 TB/s; 61 ragged sequences to 8191, groups of 8, fp16: 116 us, 5.6 TB/s; 16 ragged to 32K, 4 KV
-// heads, groups of 16, e4m3: 59 us, 2.5 TB/s (issue and latency of the conversions and products, then the joins); one
+// heads, groups of 16, e4m3: 61 us, 2.45 TB/s (issue and latency of the conversions and products, then the joins); one
 // sequence of 517: 9.6 us (latency).  DRAM reads are 1.00 of the keys and values.
 #pragma once
 
@@ -288,6 +289,7 @@ __device__ __noinline__ void join_states(const PagedArgs& a, const Join* joins, 
   }
 }
 
+// kFine: bf16 products for a float32 output.
 template <typename TQ, typename TC, int D, int NT, bool kFine>
 __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_kernel(const PagedArgs a) {
   using S = PagedShape<TQ, TC, D, NT>;
@@ -295,8 +297,7 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
   constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kDepth = S::kDepth, kRow = S::kRow, kTile = S::kTile;
   constexpr int kSub = S::kSub, kTokens = S::kTokens;
   constexpr uint32_t kAll = kSub == 2 ? ~0u : 0xffffu;
-  // terms of a weight (see the head of this file); kFine: the output is float32
-  constexpr int kTerms = std::is_same<TM, __nv_bfloat16>::value && kFine ? 3 : 2;
+  constexpr int kTerms = kFine ? 3 : 2;    // of a weight (see the head of this file)
   constexpr int kLead = 2 * kDepth - 1;    // copy groups that may be in flight behind the one that is waited for
   constexpr float kLift = kPagedLift<TM>;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -699,25 +700,24 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
           }
         copy_wait<kLead>();
         __syncwarp();
-        // O^T += V^T P^T
+        // O^T += V^T P^T, the tile's product a sum of its own
+        constexpr int kStep = S::kE4 ? 2 : 1;   // 16-column products of a load
 #pragma unroll
-        for (int j = 0; j < D / 16; j += S::kE4 ? 2 : 1)
+        for (int j = 0; j < D / 16; j += kStep) {
+          float t[kStep][NT][4];
+#pragma unroll
+          for (int h = 0; h < kStep; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) t[h][n][e] = 0;
 #pragma unroll
           for (int i = 0; i < kSub; ++i) {
-            const auto add = [&](int to, const uint32_t (&r)[4]) {
+            const auto add = [&](int h, const uint32_t (&r)[4]) {
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                if constexpr (kFine) {
-                  float t[4] = {0, 0, 0, 0};
+              for (int n = 0; n < NT; ++n)
 #pragma unroll
-                  for (int k = kTerms - 1; k >= 0; --k) mma<TM>(t, r, p[i][n][0][k], p[i][n][1][k]);
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) o[n][to][e] += t[e];
-                } else {
-#pragma unroll
-                  for (int k = 0; k < kTerms; ++k) mma<TM>(o[n][to], r, p[i][n][0][k], p[i][n][1][k]);
-                }
-              }
+                for (int k = kTerms - 1; k >= 0; --k) mma<TM>(t[h][n], r, p[i][n][0][k], p[i][n][1][k]);
             };
             uint32_t r[4];
             if constexpr (S::kE4) {
@@ -730,13 +730,20 @@ __global__ void __launch_bounds__(PagedShape<TQ, TC, D, NT>::kThreads, 1) paged_
               widen(r[1], x[2], x[3]);
               widen(r[2], y[0], y[1]);
               widen(r[3], y[2], y[3]);
-              add(j, x);
-              add(j + 1, y);
+              add(0, x);
+              add(1, y);
             } else {
               ldsm4_trans(r, vt + chunk_at<kRow>(lane_v, 2 * j) + i * 16 * kRow);
-              add(j, r);
+              add(0, r);
             }
           }
+#pragma unroll
+          for (int h = 0; h < kStep; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[n][j + h][e] += t[h][n][e];
+        }
         __syncwarp();
         issue_v(slot);
         slot = slot + 1 == kDepth ? 0 : slot + 1;
@@ -917,7 +924,9 @@ inline int paged_max_heads(int d) { return d == 64 ? 32 : d == 128 ? 24 : 16; }
 
 template <typename TQ, typename TC, int D, int NT>
 cudaError_t launch_paged_out(const PagedArgs& a, int grid, cudaStream_t s) {
-  return a.out_f32 ? launch_paged_kernel<TQ, TC, D, NT, true>(a, grid, s) : launch_paged_kernel<TQ, TC, D, NT, false>(a, grid, s);
+  if constexpr (std::is_same<TC, __nv_bfloat16>::value)
+    if (a.out_f32) return launch_paged_kernel<TQ, TC, D, NT, true>(a, grid, s);
+  return launch_paged_kernel<TQ, TC, D, NT, false>(a, grid, s);
 }
 
 template <typename TQ, typename TC>

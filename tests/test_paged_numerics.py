@@ -151,25 +151,40 @@ def test_weights_of_float32_outputs(dtype, kv, n):
     assert int(((coarse - o).abs() > tol + 2.0 ** -24 * o.abs()).sum()) > 100
 
 
-def test_sums_of_float32_outputs():
-    """Units that are one warp's each, long enough for their running sums to show: products of a tile are added by float32
-    additions, n / 16 of them for the output and as many for the sum of the weights (and one more within a tile), each off
-    by 2^-24 of what has been summed so far, on average half of the end: 2^-24 n / 16 + 2^-24 n / 32 in all, on top of the
-    above.  Sums that stay in the tensor cores from tile to tile lose several times as much, all in one direction."""
+def long_units(dtype, n, out_dtype):
+    """(out, its 64-bit value, tolerance without the output's rounding) of units that are one warp's each, n tokens long, all
+    over the same pages; values are positive, so that an error in one direction adds up.
+
+    Heads of 64 go in tiles of 32 tokens: n / 32 float32 additions of a tile's product to the output, n / 16 to a lane's sum
+    of the weights, each off by 2^-24 of what has been summed so far, on average half of the end: 2^-24 (n / 64 + n / 32)
+    on top of 4 e + 2^-20 + 5 2^-22 as above."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    Hkv, d, n = 8, 64, 4096
+    Hkv, d = 8, 64
     B = -(-12 * min(sms, 160) // Hkv)
     g = torch.Generator().manual_seed(3)
-    K = (torch.randn(n // 16, Hkv, 16, d, generator=g) / 8).to(BF).cuda()
-    V = (torch.rand(n // 16, Hkv, 16, d, generator=g) + 0.5).to(BF).cuda()
-    c = hhr.HHRPagedCache(q_heads=Hkv, kv_heads=Hkv, page=16, head_dim=d, K=K, V=V)
-    q = (torch.randn(B, Hkv, d, generator=g) / 8).to(BF).cuda()
-    table = torch.arange(n // 16, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()   # all share their pages
-    out, _, _ = attend(c, q, table, [n] * B, F32)
-    k, v = (p.double().cpu().transpose(1, 2).reshape(n, Hkv, d) for p in (K, V))
-    x = torch.einsum("bhd,nhd->bhn", q.double().cpu(), k) / 8
-    e = (torch.einsum("bhd,nhd->bhn", q.double().cpu().abs(), k.abs()) / 8).amax(-1)[..., None] * 68 * 2.0 ** -24
-    w = torch.softmax(x, -1)
-    o = torch.einsum("bhn,nhd->bhd", w, v)
-    tol = (4 * e + 2.0 ** -20 + 5 * 2.0 ** -22 + 2.0 ** -24 * (n / 16 + n / 32)) * o
-    close(out, o, tol)
+    K = (torch.randn(n // 16, Hkv, 16, d, generator=g) / 8).to(dtype).cuda()
+    V = (torch.rand(n // 16, Hkv, 16, d, generator=g) + 0.5).to(dtype).cuda()
+    c = hhr.HHRPagedCache(q_heads=Hkv, kv_heads=Hkv, page=16, head_dim=d, dtype=dtype, K=K, V=V)
+    q = (torch.randn(B, Hkv, d, generator=g) / 8).to(dtype).cuda()
+    table = torch.arange(n // 16, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+    out, _, _ = attend(c, q, table, [n] * B, out_dtype)
+    k, v = (p.double().transpose(1, 2).reshape(n, Hkv, d) for p in (K, V))
+    x = torch.einsum("bhd,nhd->bhn", q.double(), k) / 8
+    e = (torch.einsum("bhd,nhd->bhn", q.double().abs(), k.abs()) / 8).amax(-1)[..., None] * 68 * 2.0 ** -24
+    o = torch.einsum("bhn,nhd->bhd", torch.softmax(x, -1), v)
+    tol = (4 * e + 2.0 ** -20 + 5 * 2.0 ** -22 + 2.0 ** -24 * (n / 64 + n / 32)) * o
+    return out, o.cpu(), tol.cpu()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP16])
+def test_sums_of_float32_outputs(dtype):
+    """Sums that stay in the tensor cores from tile to tile lose about 1500 to 1900 2^-24 here, in one direction; the
+    tolerance is about 800."""
+    close(*long_units(dtype, 16384, F32))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP16])
+def test_sums_of_16_bit_outputs(dtype):
+    """Beside half a step of its type an output may be off by its float32 sums' tolerance, 1.9e-4 here.  Sums in the tensor
+    cores lose 2.9e-4, more than half a step of fp16."""
+    close(*long_units(dtype, 65536, dtype))
