@@ -10,6 +10,7 @@ import os
 import re
 import subprocess
 import sys
+import time
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -61,21 +62,29 @@ def up_to_date() -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
+    begun = time.time()
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     extra = ["-Xptxas", "-v"] if verbose else []
+
+    def put(made: str, to: str, t: float) -> None:
+        """A whole file, as old as the sources it was made of may be: one saved in the meantime is newer."""
+        os.utime(made, (t, t))
+        os.replace(made, to)
 
     def compile_one(src: str) -> str:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
         if not force and os.path.exists(obj) and all(os.path.getmtime(f) < os.path.getmtime(obj)
                                                      for f in _src_deps(src)):
             return obj
-        cmd = [nvcc, *ARCH, *NVFLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
+        t, made = time.time(), obj + ".tmp.o"
+        cmd = [nvcc, *ARCH, *NVFLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", made]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         if verbose:
             sys.stderr.write(r.stderr)
+        put(made, obj, t)
         return obj
 
     with ThreadPoolExecutor(len(SOURCES)) as ex:
@@ -85,7 +94,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+    put(tmp, LIB, begun)
     return LIB
 
 
