@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import math
+import threading
 
 import torch
 
@@ -62,10 +63,25 @@ class HHRPagedCache:
         self._descs = {}
         self._index, self._Hq, self._Hkv, self._d = K.get_device(), q_heads, kv_heads, head_dim
         self.workspace = self.new_workspace()
+        self._spaces, self._growing = {}, threading.Lock()
+
+    def _workspace(self):
+        """The workspace of the current stream, whose calls follow one another: `workspace` for the first one and for
+        captured calls on a stream that had none, one of its own for every other stream."""
+        if self._index < 0:
+            return self.workspace
+        stream = torch._C._cuda_getCurrentRawStream(self._index)
+        space = self._spaces.get(stream)
+        if space is None:
+            with self._growing, torch.cuda.device(self._index):
+                if torch.cuda.is_current_stream_capturing():    # (a new one would be zeros at the graph's replays only)
+                    return self.workspace
+                space = self._spaces.setdefault(stream, self.new_workspace() if self._spaces else self.workspace)
+        return space
 
     def new_workspace(self):
-        """A workspace of its own, for attend calls that may run at the same time as others on this cache (another
-        stream, another captured graph)."""
+        """A workspace of its own, for the attend calls of a captured graph that may run at the same time as others on
+        this cache."""
         ws = B.hhr_paged_workspace_size(self.desc)
         if ws == 0:
             raise B.HhrError(B.HHR_ERR_INVALID_ARG, "hhr_paged_workspace_size")
@@ -151,8 +167,8 @@ class HHRPagedCache:
         """Attention of q [B, q_heads, head_dim] over the first lens[b] (int32) tokens of
         each sequence, or the last `window` of them; into out (dtype or float32;
         a new tensor of dtype if None) and lse (float32 [B, q_heads], optional).
-        scale: 1/sqrt(head_dim) if None.  workspace (new_workspace): needed by calls that may
-        run at the same time as another one on this cache.  lens and table must not change while the call runs (hhr.h,
+        scale: 1/sqrt(head_dim) if None.  workspace (new_workspace): needed by a captured call
+        that may run at the same time as another call on this cache; calls on several streams have one each.  lens and table must not change while the call runs (hhr.h,
         hhr_paged_attend).  A serving call: it has no gradient."""
         index = self._index
         desc, rows = self._table(table)
@@ -171,7 +187,7 @@ class HHRPagedCache:
         if window >> 31:      # no sequence is that long
             window = (1 << 31) - 1 if window > 0 else -1
         if workspace is None:
-            workspace = self.workspace
+            workspace = self._workspace()
         elif workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError(f"workspace: expected a contiguous tensor on {self.device}")
         written((out,) if lse is None else (out, lse))
@@ -184,7 +200,11 @@ class HHRPagedCache:
         return out
 
     def status(self, stream=None, workspace=None) -> int:
-        """HHR_OK, or HHR_ERR_BAD_INDEX after a page, sequence or length out of range; cleared after reading."""
-        ws = self.workspace if workspace is None else workspace
+        """HHR_OK, or HHR_ERR_BAD_INDEX after a page, sequence or length out of range; cleared after reading.  Waits for
+        `stream` (the current one if None); without a workspace, that of every stream is read."""
         with torch.cuda.device(self.device):
-            return B.hhr_read_status(ws, stream)
+            if workspace is not None:
+                return B.hhr_read_status(workspace, stream)
+            with self._growing:
+                spaces = {id(w): w for w in (self.workspace, *self._spaces.values())}.values()
+            return max(B.hhr_read_status(w, stream) for w in spaces)
