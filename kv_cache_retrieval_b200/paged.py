@@ -20,6 +20,8 @@ from .rope import check_vector, fits, on_device, rotation, written
 _TYPES = {torch.bfloat16: B.HHR_TYPE_BF16, torch.float16: B.HHR_TYPE_F16, torch.float32: B.HHR_TYPE_F32,
           torch.float8_e4m3fn: B.HHR_TYPE_E4M3}
 
+_growing = threading.Lock()    # of any cache's workspaces
+
 
 class HHRPagedCache:
     def __init__(self, *, q_heads, kv_heads, pages=None, page=16, head_dim=128, dtype=torch.bfloat16,
@@ -63,7 +65,7 @@ class HHRPagedCache:
         self._descs = {}
         self._index, self._Hq, self._Hkv, self._d = K.get_device(), q_heads, kv_heads, head_dim
         self.workspace = self.new_workspace()
-        self._spaces, self._growing = {}, threading.Lock()
+        self._spaces = {}
 
     def _workspace(self):
         """The workspace of the current stream, whose calls follow one another: `workspace` for the first one and for
@@ -73,7 +75,7 @@ class HHRPagedCache:
         stream = torch._C._cuda_getCurrentRawStream(self._index)
         space = self._spaces.get(stream)
         if space is None:
-            with self._growing, torch.cuda.device(self._index):
+            with _growing, torch.cuda.device(self._index):
                 if torch.cuda.is_current_stream_capturing():    # (a new one would be zeros at the graph's replays only)
                     return self.workspace
                 space = self._spaces.setdefault(stream, self.new_workspace() if self._spaces else self.workspace)
@@ -205,6 +207,6 @@ class HHRPagedCache:
         with torch.cuda.device(self.device):
             if workspace is not None:
                 return B.hhr_read_status(workspace, stream)
-            with self._growing:
+            with _growing:
                 spaces = {id(w): w for w in (self.workspace, *self._spaces.values())}.values()
             return max(B.hhr_read_status(w, stream) for w in spaces)

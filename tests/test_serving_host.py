@@ -79,3 +79,10 @@ def test_sizes_beyond_int32_are_not_cut_off(monkeypatch):
     with pytest.raises(ValueError, match="2\\^31"):
         hhr.HHRPagedCache(q_heads=2 ** 32 + 8, kv_heads=2, pages=4, head_dim=64, device="cpu")
     assert not calls
+
+
+def test_a_cache_can_be_copied():
+    import copy
+    c = hhr.HHRPagedCache(q_heads=8, kv_heads=2, pages=4, head_dim=64, device="cpu")
+    d = copy.deepcopy(c)
+    assert d.K.data_ptr() != c.K.data_ptr() and d.desc.Hq == 8
