@@ -36,10 +36,11 @@
 // whose P never leaves its registers; the tensor pipe has room to spare (busy 18 % at 128K), and a 128-row tile with its
 // commits would couple the warps that the private rings keep apart.
 //
-// Measured (B200, captured passes): 1 x 128K, 8 KV heads of 128, bf16: 86 us, 6.25 TB/s (0.97 of the copy bandwidth);
-// 8 x 64K: 305 us, 7.0 TB/s; 61 ragged sequences to 8191, groups of 8, fp16: 116 us, 5.6 TB/s; 16 ragged to 32K, 4 KV
-// heads, groups of 16, e4m3: 61 us, 2.45 TB/s (issue and latency of the conversions and products, then the joins); one
-// sequence of 517: 9.6 us (latency).  DRAM reads are 1.00 of the keys and values.
+// Measured (B200, captured passes): 1 x 128K, 8 KV heads of 128, bf16: 87 us, 6.2 TB/s (0.95 of the copy bandwidth);
+// 8 x 64K: 305 to 312 us by the GPU, 6.9 to 7.0 TB/s; 61 ragged sequences to 8191, groups of 8, fp16: 119 us, 5.5 TB/s;
+// 16 ragged to 32K, 4 KV heads, groups of 16, e4m3: 61 us, 2.45 TB/s (issue and latency of the conversions and products,
+// then the joins); one sequence of 517: 10 us (latency, and the launch arguments that every thread copies to local memory
+// for the join, 12.7 MB a call).  DRAM reads are 1.00 of the keys and values.
 #pragma once
 
 #include <algorithm>
@@ -65,7 +66,8 @@ struct PagedShape {
   static constexpr int kTile = kTokens * kRow;
   static constexpr int kHeads = 8 * NT;
   // Registers hold the query fragments of 8 heads; those of more are read from shared memory, each warp its own copy
-  // (16 heads, d = 128, 8-bit, one term a weight: 58 us in registers of 8 warps, 55 of 12 warps, 53 from shared memory).
+  // (16 heads, d = 128, 8-bit, one term a weight: 58 us in registers of 8 warps, 55 of 12 warps, 53 from shared memory;
+  // the variants of 16 and more heads spill 4 to 56 bytes a thread all the same).
   static constexpr bool kQRegs = NT == 1;
   // More warps hide more latency where their registers allow it.  The rings together hold about 100 KB: with 192 KB in
   // flight the SMs at the head of their group run 25 % ahead of the last ones and the call waits for those (8 sequences

@@ -121,7 +121,8 @@ class _Rope(torch.autograd.Function):
 def rope(x, positions, freqs, *, interleaved=False, mscale=1.0, out=None):
     """x [T, H, d] (bf16, fp16 or fp32; any token and head strides) with its first 2 * freqs.numel() elements
     rotated by positions[t] * freqs (hhr_rope).  positions: int32 [T]; freqs: float64 [rot/2].  Differentiable
-    with respect to x, backward and forward (dual tensors).  out: where to put the result (x itself rotates in place); not with a gradient."""
+    with respect to x, backward and forward (dual tensors).  out: where to put the result (x itself rotates in place; no other
+    overlap with x); not with a gradient."""
     shape = x.shape
     if len(shape) != 3 or x.dtype not in _TYPES or not x.is_cuda:
         raise ValueError(f"x: expected a bf16, fp16 or fp32 CUDA tensor [T, H, d], got {x.dtype} {tuple(x.shape)} on {x.device}")
