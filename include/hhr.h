@@ -487,8 +487,9 @@ size_t hhr_paged_workspace_size(const hhr_paged* cache);
  * changed under it ends with outputs of no meaning, and its workspace has to be
  * zero-filled again before the next one.
  * Supported: B * Hq < 2^31, B * Hq * table_cols * page < 2^40.  scale: any
- * value for which scale * k_scale * log2(e) is finite in float32.  A logit of -inf leaves its token out; other non-finite values
- * among a sequence's tokens make its outputs non-finite.
+ * value for which scale * k_scale * log2(e) is finite in float32.  A logit of
+ * -inf leaves its token out; other non-finite values among a sequence's tokens
+ * make its outputs non-finite.
  * A length outside [0, table_cols * page] counts as 0 and a page outside
  * [0, n_pages) as masked tokens; either sets the workspace status word to
  * HHR_ERR_BAD_INDEX (hhr_read_status) and leaves the workspace usable.

@@ -127,7 +127,7 @@ class HHRPagedCache:
         (rows of `table`; None: token t of sequence t).  freqs (rope_freqs): the keys
         are rotated by rope_positions (None: positions) on the way, and with q
         [T, q_heads, head_dim] the queries too, into q_out (a new tensor if
-        None; q itself rotates in place).  Returns q_out.  Writes the pools in place: no
+        None, whose skipped rows hold nothing in particular; q itself rotates in place).  Returns q_out.  Writes the pools in place: no
         gradient passes through it."""
         index = self._index
         desc, rows = self._table(table)
@@ -169,9 +169,9 @@ class HHRPagedCache:
         """Attention of q [B, q_heads, head_dim] over the first lens[b] (int32) tokens of
         each sequence, or the last `window` of them; into out (dtype or float32;
         a new tensor of dtype if None) and lse (float32 [B, q_heads], optional).
-        scale: 1/sqrt(head_dim) if None.  workspace (new_workspace): needed by a captured call
-        that may run at the same time as another call on this cache; calls on several streams have one each.  lens and table must not change while the call runs (hhr.h,
-        hhr_paged_attend).  A serving call: it has no gradient."""
+        scale: 1/sqrt(head_dim) if None.  workspace (new_workspace): needed by a captured call that may run
+        at the same time as another call on this cache; calls on several streams have one each.  lens and table
+        must not change while the call runs (hhr.h, hhr_paged_attend).  A serving call: it has no gradient."""
         index = self._index
         desc, rows = self._table(table)
         q_B, q_seq = self._rows("q", q, self._Hq)

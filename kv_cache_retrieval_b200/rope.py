@@ -45,7 +45,7 @@ def check_vector(name, t, dtype, length, index):
 
 def fits(*sizes):
     """The sizes, which the library takes as int32: ctypes would drop the bits beyond."""
-    if any(n >> 31 for n in sizes):
+    if max(sizes) >> 31 > 0:
         raise ValueError(f"sizes of 2^31 and more: {sizes}")
     return sizes
 
@@ -121,8 +121,9 @@ class _Rope(torch.autograd.Function):
 def rope(x, positions, freqs, *, interleaved=False, mscale=1.0, out=None):
     """x [T, H, d] (bf16, fp16 or fp32; any token and head strides) with its first 2 * freqs.numel() elements
     rotated by positions[t] * freqs (hhr_rope).  positions: int32 [T]; freqs: float64 [rot/2].  Differentiable
-    with respect to x, backward and forward (dual tensors).  out: where to put the result (x itself rotates in place; no other
-    overlap with x); not with a gradient."""
+    with respect to x, backward and forward (dual tensors).  out: where to put the result (x itself rotates in
+    place; no other overlap with x); not with a gradient.  Captured into a CUDA graph, a backward pass wants leaves
+    that no live eager graph holds: torch orders it behind that graph's stream."""
     shape = x.shape
     if len(shape) != 3 or x.dtype not in _TYPES or not x.is_cuda:
         raise ValueError(f"x: expected a bf16, fp16 or fp32 CUDA tensor [T, H, d], got {x.dtype} {tuple(x.shape)} on {x.device}")
